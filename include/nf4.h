@@ -3,8 +3,9 @@
  * quantization of the absmax constants, dequantization, and the 4-bit-weight x
  * bf16-activation matmul that dequantizes on the fly (GEMV for decode, also
  * grouped over weights that share an input; GEMM for prefill, also with a
- * low-rank adapter in the same accumulator; and the GEMM's input gradient
- * through the frozen weight), for NVIDIA B200 (sm_100a).
+ * low-rank adapter in the same accumulator; the GEMM's input gradient through
+ * the frozen weight; and both grouped by expert), and weights of uniform 4-bit
+ * codes with group scales with their decode product, for NVIDIA B200 (sm_100a).
  *
  * Method sources (web pages on bitsandbytes / QLoRA):
  *   [bnb-tools] "bitsandbytes" (ozercemkelahmet.com/tools/bitsandbytes):
@@ -61,7 +62,8 @@ typedef enum {
   NF4_ERR_TIMEOUT = 6      /* a device-side wait gave up (see nf4_check_device_error) */
 } nf4_status;
 
-typedef enum { NF4_F32 = 0, NF4_BF16 = 1 } nf4_dtype;
+/* NF4_F16 is taken by the group-scale functions (nf4_*_groups) only. */
+typedef enum { NF4_F32 = 0, NF4_BF16 = 1, NF4_F16 = 2 } nf4_dtype;
 
 /* 8-bit code of the double-quantized absmax constants.
  * NF4_DQ_E4M3: OCP FP8 E4M3 ("float8", [bnb-tut] "How NF4 Works"), top code 448.
@@ -330,6 +332,89 @@ NF4_API size_t nf4_gemm_lora_workspace_bytes(const nf4_weight *w, int64_t m);
 NF4_API nf4_status nf4_gemm_dx(const nf4_weight *w, const void *dy, int64_t m, void *dx, void *workspace,
                        size_t workspace_bytes, nf4_stream_t stream);
 NF4_API size_t nf4_gemm_dx_workspace_bytes(const nf4_weight *w, int64_t m);
+
+/* nf4_gemm grouped by expert, for the linear layers of a mixture-of-experts
+ * block whose experts are frozen 4-bit weights: the rows of X are sorted by
+ * expert, and each is multiplied by its own expert's weight,
+ *   Y[t, n] = bf16_rn( sum_k Wc[e * N + n, k] * X[t, k] ),
+ *   offsets[e] <= t < offsets[e + 1],
+ * with Wc as in nf4_gemv, accumulated in fp32.  One launch; the numbers of
+ * rows are read on the GPU, so a router's counts need no copy to the host.
+ *   w        the experts' weights stacked: rows = experts * N, cols = K, NF4
+ *            or FP4, plain or double-quantized scales (one record for the
+ *            stack); N % 128 == 0, K % 64 == 0 (else NF4_ERR_UNSUPPORTED)
+ *   experts  1 .. NF4_EXPERTS_MAX
+ *   x        device bf16 [m, K];  y  device bf16 [m, N];  m >= 0
+ *   offsets  device int32 [experts + 1], 4-byte aligned, never decreasing,
+ *            within 0 .. m: expert e has rows offsets[e] .. offsets[e + 1] - 1
+ *            (possibly none).  Rows before offsets[0] and from
+ *            offsets[experts] on belong to no expert; their outputs are left
+ *            as they were.  Values outside 0 .. m are held to that range;
+ *            where offsets decrease, which rows are written is unspecified.
+ *   workspace  device scratch of nf4_gemm_experts_workspace_bytes(w, experts,
+ *            m) bytes, with nf4_gemm's contract (may be NULL when 0;
+ *            zero-filled before its first use, left ready by every completed
+ *            call; separate buffers for calls that may overlap). */
+#define NF4_EXPERTS_MAX 256
+NF4_API nf4_status nf4_gemm_experts(const nf4_weight *w, int32_t experts, const void *x, const int32_t *offsets,
+                                    int64_t m, void *y, void *workspace, size_t workspace_bytes,
+                                    nf4_stream_t stream);
+NF4_API size_t nf4_gemm_experts_workspace_bytes(const nf4_weight *w, int32_t experts, int64_t m);
+
+/* Input gradient of nf4_gemm_experts:
+ *   dX[t, k] = bf16_rn( sum_n dY[t, n] * Wc[e * N + n, k] )
+ * for the rows of each expert, accumulated in fp32, the stacked weight read as
+ * it lies.  Arguments as in nf4_gemm_experts with dy [m, N] and dx [m, K];
+ * N % 64 == 0, K % 128 == 0 (else NF4_ERR_UNSUPPORTED). */
+NF4_API nf4_status nf4_gemm_experts_dx(const nf4_weight *w, int32_t experts, const void *dy, const int32_t *offsets,
+                                       int64_t m, void *dx, void *workspace, size_t workspace_bytes,
+                                       nf4_stream_t stream);
+NF4_API size_t nf4_gemm_experts_dx_workspace_bytes(const nf4_weight *w, int32_t experts, int64_t m);
+
+/* A weight of uniform 4-bit codes with group scales: value s (q - z), with one
+ * 16-bit scale s and one zero point z (0..15) per `group` consecutive columns
+ * of a row.  All pointers are device pointers.
+ *   packed  [rows, cols / 2] bytes, 16-byte aligned: eight codes of a row per
+ *           little-endian 32-bit word, code j in nibble j / 2 of the word's
+ *           low half for even j and of its high half for odd j
+ *   scale   [rows, cols / group] of scale_dtype (NF4_BF16 or NF4_F16)
+ *   zero    [rows, cols / group] bytes 0..15, or NULL: 8 everywhere
+ *   group   32, 64 or 128, dividing cols (else NF4_ERR_UNSUPPORTED)
+ * rows need no alignment. */
+typedef struct {
+  const uint8_t *packed;
+  const void *scale;
+  const uint8_t *zero;
+  int64_t rows, cols;
+  int32_t group, scale_dtype;
+} nf4_group_weight;
+
+/* Quantization to uniform 4-bit codes, each step rounded once in fp32.  Per
+ * group, with T() the rounding to scale_dtype (kept finite) and rint() to the
+ * nearest integer, ties to even:
+ *   zero_out given  lo = min(0, min w), hi = max(0, max w),
+ *                   s = T((hi - lo) / 15), z = min(rint(-lo / s), 15)
+ *   zero_out NULL   s = T(max |w| / 7), z = 8
+ *   q = rint(w / s) + z, held to 0..15;  where s == 0, q = z (and z = 0 if
+ *   stored)
+ *   src  device [rows, cols] of src_dtype (NF4_F32, NF4_BF16 or NF4_F16),
+ *        16-byte aligned, |w| <= 1e38;  the outputs as in nf4_group_weight. */
+NF4_API nf4_status nf4_quantize_groups(const void *src, int32_t src_dtype, int64_t rows, int64_t cols, int32_t group,
+                                       int32_t scale_dtype, uint8_t *packed_out, void *scale_out, uint8_t *zero_out,
+                                       nf4_stream_t stream);
+
+/* Expansion: out = s (q - z), exact in fp32 and rounded once to out_dtype.
+ *   out  device [rows, cols] of out_dtype (NF4_F32, NF4_BF16 or NF4_F16), 16-byte aligned */
+NF4_API nf4_status nf4_dequantize_groups(const nf4_group_weight *w, void *out, int32_t out_dtype, nf4_stream_t stream);
+
+/* Decode product with group scales:
+ *   y[b, n] = T( sum_g s[n, g] * sum_{k in g} (q[n, k] - z[n, g]) * x[b, k] )
+ * with fp32 sums; unlike nf4_gemv's, the weight is not rounded to 16 bits
+ * before the product.
+ *   x  device [batch, cols], y  device [batch, rows] (2-byte aligned), both of
+ *   w->scale_dtype;  1 <= batch <= 8. */
+NF4_API nf4_status nf4_gemv_groups(const nf4_group_weight *w, const void *x, int32_t batch, void *y,
+                                   nf4_stream_t stream);
 
 /* Bytes of a quantized tensor of n elements: ceil(n/2) codes + either
  * 4*ceil(n/blocksize) (fp32 absmax) or ceil(n/blocksize) 8-bit codes +

@@ -13,6 +13,7 @@ Typical use:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional
@@ -20,11 +21,13 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import NF4_BF16, NF4_DQ_E4M3, NF4_DQ_INT8, NF4_F32, NF4_QUANT_FP4, NF4_QUANT_NF4, NF4Error
+from ._lib import NF4_BF16, NF4_DQ_E4M3, NF4_DQ_INT8, NF4_F16, NF4_F32, NF4_QUANT_FP4, NF4_QUANT_NF4, NF4Error
 
 __all__ = ["QuantizedWeight", "quantize", "double_quant", "quantize_weight", "dequantize", "gemv", "gemm",
            "storage_bytes", "gemm_workspace_bytes", "gemm_dx", "gemm_dx_workspace_bytes", "gemm_lora", "gemv_grouped", "gemv_stream",
            "double_quant_many", "quantize_many",
+           "gemm_experts", "gemm_experts_workspace_bytes", "gemm_experts_dx", "gemm_experts_dx_workspace_bytes",
+           "GroupWeight", "quantize_groups", "dequantize_groups", "gemv_groups",
            "gemm_lora_workspace_bytes", "code_table", "check_device_error", "kernel_launches", "NF4Error", "library_path"]
 
 BLOCKSIZE = 64
@@ -52,6 +55,17 @@ def _need_cuda(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _on_device(device: torch.device):
+    """The CUDA device of the tensors as the current one (a no-op when it already is)."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _need_out(out: torch.Tensor, shape, dtype: torch.dtype, device: torch.device) -> None:
+    _need_cuda(out, "out")
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 @dataclass
@@ -355,6 +369,168 @@ def gemm_dx_workspace_bytes(qw: QuantizedWeight, m: int) -> int:
     """Scratch bytes nf4_gemm_dx needs for `m` gradient rows (0 when none)."""
     d = qw.descriptor()
     return int(_lib.load().nf4_gemm_dx_workspace_bytes(ctypes.byref(d), m))
+
+
+def _experts(name: str, qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int, gradient: bool,
+             out, workspace, stream) -> torch.Tensor:
+    for t, what in ((x, "dy" if gradient else "x"), (offsets, "offsets")):
+        _need_cuda(t, what)
+        if t.device != qw.packed.device:
+            raise ValueError(f"{what} must be on the weight's device")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("activations must be bfloat16")
+    if offsets.dtype != torch.int32 or offsets.numel() != experts + 1:
+        raise ValueError("offsets must be int32 with experts + 1 entries")
+    if experts < 1 or qw.rows % experts:
+        raise ValueError("the weight's rows must be a multiple of experts")
+    n = qw.rows // experts
+    width, owidth = (n, qw.cols) if gradient else (qw.cols, n)
+    if x.dim() < 1 or x.shape[-1] != width:
+        raise ValueError(f"the activations' last dimension must be {width}")
+    m = x.numel() // width if width else 0
+    with _on_device(x.device):
+        lib = _lib.load()
+        d = qw.descriptor()
+        if out is None:
+            out = torch.empty(m, owidth, dtype=torch.bfloat16, device=x.device)
+        else:
+            _need_out(out, (m, owidth), torch.bfloat16, x.device)
+        ws_bytes = getattr(lib, name + "_workspace_bytes")(ctypes.byref(d), experts, m)
+        if workspace is None and ws_bytes:
+            workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=x.device)  # zeroed once, then reusable
+        st = getattr(lib, name)(ctypes.byref(d), experts, _ptr(x), _ptr(offsets), m, _ptr(out), _ptr(workspace),
+                                workspace.numel() if workspace is not None else 0, _stream(stream))
+        _lib.check(st, name)
+    return out
+
+
+def gemm_experts(qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int, out=None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = bf16(Wc_e X[t]) for the rows offsets[e] <= t < offsets[e + 1] of each expert e: ``gemm`` grouped by
+    expert, the row counts read on the GPU.
+
+    qw stacks the experts' weights (rows = experts * N); x is bf16 [m, cols], sorted by expert; offsets is int32
+    [experts + 1] on the GPU.  Rows that no expert has are left unwritten (undefined in a fresh output)."""
+    return _experts("nf4_gemm_experts", qw, x, offsets, experts, False, out, workspace, stream)
+
+
+def gemm_experts_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
+    """Scratch bytes nf4_gemm_experts needs for `m` rows in all (0 when none)."""
+    d = qw.descriptor()
+    return int(_lib.load().nf4_gemm_experts_workspace_bytes(ctypes.byref(d), experts, m))
+
+
+def gemm_experts_dx(qw: QuantizedWeight, dy: torch.Tensor, offsets: torch.Tensor, experts: int, out=None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Input gradient of ``gemm_experts``: dX[t] = bf16(Wc_e^T dY[t]) for dY bf16 [m, N] sorted by expert."""
+    return _experts("nf4_gemm_experts_dx", qw, dy, offsets, experts, True, out, workspace, stream)
+
+
+def gemm_experts_dx_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
+    """Scratch bytes nf4_gemm_experts_dx needs for `m` rows in all (0 when none)."""
+    d = qw.descriptor()
+    return int(_lib.load().nf4_gemm_experts_dx_workspace_bytes(ctypes.byref(d), experts, m))
+
+
+_FLOAT_CODES = {torch.float32: NF4_F32, torch.bfloat16: NF4_BF16, torch.float16: NF4_F16}
+
+
+@dataclass
+class GroupWeight:
+    """A weight [rows, cols] of uniform 4-bit codes with group scales: value scale * (code - zero), one scale
+    (bf16 or fp16 [rows, cols / group]) and one zero point (uint8 0..15, or zero=None: 8 everywhere) per group of
+    32, 64 or 128 columns.  packed holds eight codes per 32-bit word: code j in nibble j / 2 of the word's low half
+    (j even) or high half (j odd)."""
+    packed: torch.Tensor
+    scale: torch.Tensor
+    zero: Optional[torch.Tensor]
+    rows: int
+    cols: int
+    group: int = 128
+
+    def descriptor(self) -> _lib.NF4GroupWeight:
+        if self.scale.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("scale must be bfloat16 or float16")
+        groups = self.rows * (self.cols // self.group) if self.group > 0 else 0
+        for t, name, n in ((self.packed, "packed", self.rows * self.cols // 2), (self.scale, "scale", groups),
+                           (self.zero, "zero", groups)):
+            if t is None:
+                continue
+            _need_cuda(t, name)
+            if t.device != self.packed.device:
+                raise ValueError(f"{name} must be on the weight's device")
+            if t.numel() != n:
+                raise ValueError(f"{name} must have {n} entries")
+        for t, name in ((self.packed, "packed"), (self.zero, "zero")):
+            if t is not None and t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be uint8")
+        return _lib.NF4GroupWeight(_ptr(self.packed), _ptr(self.scale), _ptr(self.zero), self.rows, self.cols,
+                                   self.group, _FLOAT_CODES[self.scale.dtype])
+
+
+def quantize_groups(w: torch.Tensor, group: int = 128, symmetric: bool = False,
+                    scale_dtype: Optional[torch.dtype] = None, stream=None) -> GroupWeight:
+    """Quantize a 2-D weight [rows, cols] (fp32, bf16 or fp16) to uniform 4-bit codes with one scale and, unless
+    `symmetric`, one zero point per `group` columns.  scale_dtype: bf16 or fp16 (default: w's type, bf16 for fp32);
+    it is also the activations' type in gemv_groups."""
+    _need_cuda(w, "w")
+    if w.dim() != 2:
+        raise ValueError("quantize_groups takes a 2-D [rows, cols] tensor")
+    if w.dtype not in _FLOAT_CODES:
+        raise TypeError("quantize_groups takes float32, bfloat16 or float16")
+    if scale_dtype is None:
+        scale_dtype = torch.float16 if w.dtype == torch.float16 else torch.bfloat16
+    if scale_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("scale_dtype must be bfloat16 or float16")
+    rows, cols = w.shape
+    if group not in (32, 64, 128) or cols % group:
+        raise ValueError("group must be 32, 64 or 128 and divide cols")
+    with _on_device(w.device):
+        packed = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
+        scale = torch.empty(rows, cols // group, dtype=scale_dtype, device=w.device)
+        zero = None if symmetric else torch.empty(rows, cols // group, dtype=torch.uint8, device=w.device)
+        st = _lib.load().nf4_quantize_groups(_ptr(w), _FLOAT_CODES[w.dtype], rows, cols, group,
+                                             _FLOAT_CODES[scale_dtype], _ptr(packed), _ptr(scale), _ptr(zero),
+                                             _stream(stream))
+        _lib.check(st, "nf4_quantize_groups")
+    return GroupWeight(packed=packed, scale=scale, zero=zero, rows=rows, cols=cols, group=group)
+
+
+def dequantize_groups(gw: GroupWeight, dtype: torch.dtype = torch.float32, out=None, stream=None) -> torch.Tensor:
+    """Expand a GroupWeight to fp32, bf16 or fp16 [rows, cols]."""
+    if dtype not in _FLOAT_CODES:
+        raise TypeError("dequantize_groups produces float32, bfloat16 or float16")
+    d = gw.descriptor()
+    with _on_device(gw.packed.device):
+        if out is None:
+            out = torch.empty(gw.rows, gw.cols, dtype=dtype, device=gw.packed.device)
+        else:
+            _need_out(out, (gw.rows, gw.cols), dtype, gw.packed.device)
+        st = _lib.load().nf4_dequantize_groups(ctypes.byref(d), _ptr(out), _FLOAT_CODES[dtype], _stream(stream))
+        _lib.check(st, "nf4_dequantize_groups")
+    return out
+
+
+def gemv_groups(gw: GroupWeight, x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """y[b, n] = sum_k scale * (code - zero) * x[b, k] for x [B, cols] of the scales' type, 1 <= B <= 8; fp32 sums,
+    the weight not rounded to 16 bits."""
+    _need_cuda(x, "x")
+    if x.dtype != gw.scale.dtype:
+        raise TypeError("x must have the scales' type")
+    if x.device != gw.packed.device:
+        raise ValueError("x must be on the weight's device")
+    if x.dim() < 1 or x.shape[-1] != gw.cols:
+        raise ValueError("x must have cols columns")
+    d = gw.descriptor()
+    batch = x.numel() // gw.cols if gw.cols else x.shape[:-1].numel()
+    with _on_device(x.device):
+        if out is None:
+            out = torch.empty(batch, gw.rows, dtype=x.dtype, device=x.device)
+        else:
+            _need_out(out, (batch, gw.rows), x.dtype, x.device)
+        st = _lib.load().nf4_gemv_groups(ctypes.byref(d), _ptr(x), batch, _ptr(out), _stream(stream))
+        _lib.check(st, "nf4_gemv_groups")
+    return out
 
 
 def storage_bytes(n: int, use_double_quant: bool = True) -> int:

@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_PKG, "libnf4.so")
 NF4_OK = 0
 STATUS_NAMES = {0: "NF4_OK", 1: "NF4_ERR_INVALID_ARG", 2: "NF4_ERR_MISALIGNED", 3: "NF4_ERR_UNSUPPORTED",
                 4: "NF4_ERR_ARCH", 5: "NF4_ERR_CUDA", 6: "NF4_ERR_TIMEOUT"}
-NF4_F32, NF4_BF16 = 0, 1
+NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 NF4_DQ_E4M3, NF4_DQ_INT8 = 0, 1
 NF4_QUANT_NF4, NF4_QUANT_FP4 = 0, 1
 
@@ -35,6 +35,12 @@ class NF4Weight(ctypes.Structure):
 class NF4Lora(ctypes.Structure):
     """Mirror of the C struct nf4_lora."""
     _fields_ = [("down", P), ("up", P), ("r", I32), ("scale", ctypes.c_float)]
+
+
+class NF4GroupWeight(ctypes.Structure):
+    """Mirror of the C struct nf4_group_weight."""
+    _fields_ = [("packed", P), ("scale", P), ("zero", P), ("rows", I64), ("cols", I64), ("group", I32),
+                ("scale_dtype", I32)]
 
 
 SIGNATURES = {
@@ -58,6 +64,13 @@ SIGNATURES = {
     "nf4_gemm_lora_workspace_bytes": (SZ, [ctypes.POINTER(NF4Weight), I64]),
     "nf4_gemm_dx": (ctypes.c_int, [ctypes.POINTER(NF4Weight), P, I64, P, P, SZ, P]),
     "nf4_gemm_dx_workspace_bytes": (SZ, [ctypes.POINTER(NF4Weight), I64]),
+    "nf4_gemm_experts": (ctypes.c_int, [ctypes.POINTER(NF4Weight), I32, P, P, I64, P, P, SZ, P]),
+    "nf4_gemm_experts_workspace_bytes": (SZ, [ctypes.POINTER(NF4Weight), I32, I64]),
+    "nf4_gemm_experts_dx": (ctypes.c_int, [ctypes.POINTER(NF4Weight), I32, P, P, I64, P, P, SZ, P]),
+    "nf4_gemm_experts_dx_workspace_bytes": (SZ, [ctypes.POINTER(NF4Weight), I32, I64]),
+    "nf4_quantize_groups": (ctypes.c_int, [P, I32, I64, I64, I32, I32, P, P, P, P]),
+    "nf4_dequantize_groups": (ctypes.c_int, [ctypes.POINTER(NF4GroupWeight), P, I32, P]),
+    "nf4_gemv_groups": (ctypes.c_int, [ctypes.POINTER(NF4GroupWeight), P, I32, P, P]),
     "nf4_storage_bytes": (SZ, [I64, I32, I32, I32]),
     "nf4_check_device_error": (ctypes.c_int, [P]),
     "nf4_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,7 +1,8 @@
 // api.cu -- extern "C" entry points of libnf4 (declared in include/nf4.h).
 // Host-side validation happens before any launch; kernels live in the other
 // translation units (quantize.cu, double_quant.cu, dequantize.cu, gemv.cu,
-// gemv_stream.cu, gemm_sm100.cu, gemm_dx_sm100.cu, lora_down.cu).
+// gemv_stream.cu, gemm_sm100.cu, gemm_dx_sm100.cu, lora_down.cu,
+// gemm_experts_sm100.cu, gemm_experts_dx_sm100.cu, group_quant.cu, gemv_groups.cu).
 #include <atomic>
 #include <mutex>
 
@@ -486,6 +487,140 @@ nf4_status nf4_selftest_wait_timeout(nf4_stream_t stream) {
   nf4_status st = device_info(&d);
   if (st != NF4_OK) return st;
   return from_cuda(nf4::launch_wait_timeout(d.error_word, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// products grouped by expert
+
+static_assert(NF4_EXPERTS_MAX == nf4::kMaxExperts, "expert limit");
+
+namespace {
+
+// Shape rules shared by the forward product (out_tile = rows, red = cols) and the gradient (the other way round);
+// on NF4_OK with *empty false, `c` holds everything but the pointers.
+nf4_status check_experts(const nf4_weight* w, int32_t experts, int64_t m, bool gradient, nf4::ExpertsCall* c,
+                         bool* empty) {
+  nf4_status st = check_weight(w, &c->scales);
+  if (st != NF4_OK) return st;
+  if (experts < 1 || experts > NF4_EXPERTS_MAX || m < 0 || w->rows % experts != 0) return NF4_ERR_INVALID_ARG;
+  c->packed = w->packed;
+  c->experts = experts;
+  c->rows = w->rows / experts;
+  c->cols = w->cols;
+  c->m = m;
+  const int64_t out = gradient ? c->cols : c->rows, red = gradient ? c->rows : c->cols;
+  if (out % 128 != 0 || red % 64 != 0) return NF4_ERR_UNSUPPORTED;
+  *empty = m == 0 || w->rows == 0 || w->cols == 0;
+  if (*empty) return NF4_OK;
+  // tensor-map coordinates and unit numbers are 32-bit
+  if (w->rows > INT32_MAX || w->cols > INT32_MAX || m > INT32_MAX) return NF4_ERR_UNSUPPORTED;
+  if ((m / 64 + experts) * (out / 128) > INT32_MAX / 2) return NF4_ERR_UNSUPPORTED;
+  return NF4_OK;
+}
+
+using ExpertsLauncher = cudaError_t (*)(const nf4::ExpertsCall&, unsigned*, cudaStream_t, int);
+
+nf4_status run_experts(const nf4_weight* w, int32_t experts, const void* in, const int32_t* offsets, int64_t m,
+                       void* out, void* workspace, size_t workspace_bytes, bool gradient, ExpertsLauncher launch,
+                       nf4_stream_t stream) {
+  nf4::ExpertsCall c;
+  bool empty = false;
+  nf4_status st = check_experts(w, experts, m, gradient, &c, &empty);
+  if (st != NF4_OK || empty) return st;
+  if (in == nullptr || offsets == nullptr || out == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned(in, 16) || !aligned(out, 16) || !aligned(offsets, 4)) return NF4_ERR_MISALIGNED;
+  (void)workspace;
+  (void)workspace_bytes;
+  c.in = in;
+  c.offsets = offsets;
+  c.out = out;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != NF4_OK) return st;
+  return from_cuda(launch(c, d.error_word, reinterpret_cast<cudaStream_t>(stream), d.num_sms));
+}
+
+// a group-scale weight's fields; `zero` may be null (symmetric)
+nf4_status check_group_weight(const uint8_t* packed, const void* scale, const uint8_t* zero, int64_t rows,
+                              int64_t cols, int32_t group, int32_t scale_dtype, nf4::GroupWeight* g) {
+  if (rows < 0 || cols < 0) return NF4_ERR_INVALID_ARG;
+  if (scale_dtype != NF4_BF16 && scale_dtype != NF4_F16) return NF4_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return NF4_ERR_UNSUPPORTED;
+  if (cols % group != 0) return NF4_ERR_UNSUPPORTED;
+  if (cols > 0 && rows > INT64_MAX / 4 / cols) return NF4_ERR_INVALID_ARG;
+  *g = nf4::GroupWeight{packed, scale, zero, rows, cols, group, scale_dtype == NF4_F16};
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (packed == nullptr || scale == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned(packed, 16) || !aligned(scale, 2)) return NF4_ERR_MISALIGNED;
+  return NF4_OK;
+}
+
+bool float_dtype(int32_t t) { return t == NF4_F32 || t == NF4_BF16 || t == NF4_F16; }
+
+}  // namespace
+
+extern "C" {
+
+size_t nf4_gemm_experts_workspace_bytes(const nf4_weight* /*w*/, int32_t /*experts*/, int64_t /*m*/) { return 0; }
+
+size_t nf4_gemm_experts_dx_workspace_bytes(const nf4_weight* /*w*/, int32_t /*experts*/, int64_t /*m*/) { return 0; }
+
+nf4_status nf4_gemm_experts(const nf4_weight* w, int32_t experts, const void* x, const int32_t* offsets, int64_t m,
+                            void* y, void* workspace, size_t workspace_bytes, nf4_stream_t stream) {
+  return run_experts(w, experts, x, offsets, m, y, workspace, workspace_bytes, false, nf4::launch_gemm_experts, stream);
+}
+
+nf4_status nf4_gemm_experts_dx(const nf4_weight* w, int32_t experts, const void* dy, const int32_t* offsets, int64_t m,
+                               void* dx, void* workspace, size_t workspace_bytes, nf4_stream_t stream) {
+  return run_experts(w, experts, dy, offsets, m, dx, workspace, workspace_bytes, true, nf4::launch_gemm_experts_dx,
+                     stream);
+}
+
+nf4_status nf4_quantize_groups(const void* src, int32_t src_dtype, int64_t rows, int64_t cols, int32_t group,
+                               int32_t scale_dtype, uint8_t* packed_out, void* scale_out, uint8_t* zero_out,
+                               nf4_stream_t stream) {
+  nf4::GroupWeight g;
+  nf4_status st = check_group_weight(packed_out, scale_out, zero_out, rows, cols, group, scale_dtype, &g);
+  if (st != NF4_OK) return st;
+  if (!float_dtype(src_dtype)) return NF4_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (src == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned(src, 16)) return NF4_ERR_MISALIGNED;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != NF4_OK) return st;
+  return from_cuda(
+      nf4::launch_quantize_groups(src, src_dtype, g, reinterpret_cast<cudaStream_t>(stream), d.num_sms));
+}
+
+nf4_status nf4_dequantize_groups(const nf4_group_weight* w, void* out, int32_t out_dtype, nf4_stream_t stream) {
+  if (w == nullptr) return NF4_ERR_INVALID_ARG;
+  nf4::GroupWeight g;
+  nf4_status st = check_group_weight(w->packed, w->scale, w->zero, w->rows, w->cols, w->group, w->scale_dtype, &g);
+  if (st != NF4_OK) return st;
+  if (!float_dtype(out_dtype)) return NF4_ERR_INVALID_ARG;
+  if (w->rows == 0 || w->cols == 0) return NF4_OK;
+  if (out == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned(out, 16)) return NF4_ERR_MISALIGNED;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != NF4_OK) return st;
+  return from_cuda(
+      nf4::launch_dequantize_groups(g, out, out_dtype, reinterpret_cast<cudaStream_t>(stream), d.num_sms));
+}
+
+nf4_status nf4_gemv_groups(const nf4_group_weight* w, const void* x, int32_t batch, void* y, nf4_stream_t stream) {
+  if (w == nullptr) return NF4_ERR_INVALID_ARG;
+  nf4::GroupWeight g;
+  nf4_status st = check_group_weight(w->packed, w->scale, w->zero, w->rows, w->cols, w->group, w->scale_dtype, &g);
+  if (st != NF4_OK) return st;
+  if (batch < 1 || batch > 8) return NF4_ERR_INVALID_ARG;
+  if (w->rows == 0 || w->cols == 0) return NF4_OK;
+  if (w->rows > INT32_MAX || w->cols > INT32_MAX) return NF4_ERR_UNSUPPORTED;
+  if (x == nullptr || y == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(y, 2)) return NF4_ERR_MISALIGNED;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != NF4_OK) return st;
+  return from_cuda(nf4::launch_gemv_groups(g, x, batch, y, reinterpret_cast<cudaStream_t>(stream), d.num_sms));
 }
 
 }  // extern "C"

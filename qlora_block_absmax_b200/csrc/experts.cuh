@@ -1,0 +1,131 @@
+// experts.cuh -- what the expert products (gemm_experts_sm100.cu, gemm_experts_dx_sm100.cu) share: the schedule of
+// ragged tiles, the activation-tile loads and the epilogue.
+//
+// Rows [offsets[e], offsets[e + 1]) of the activations belong to expert e, whose weight is rows [e * N, (e + 1) * N)
+// of one stacked 4-bit weight.  The offsets are read on the GPU, so a launch does not know its tiles: every CTA reads
+// them, counts each expert's tiles and walks the units u = blockIdx.x, + gridDim.x, ... of the same list.  An expert of
+// m rows has ceil(m / TM) row tiles of equal width (a multiple of 16, the UMMA N); rows of a tile past the expert's
+// last one belong to another expert, are multiplied along and never stored.
+#pragma once
+#include "nf4_common.cuh"
+#include "nf4_decode.cuh"
+#include "internal.h"
+#include "umma.cuh"
+
+namespace nf4 {
+namespace experts {
+
+using namespace umma;
+
+// In shared memory, filled once per launch.
+struct Schedule {
+  int first[kMaxExperts + 1];  // first unit of expert e; first[experts] = all units
+  int row[kMaxExperts + 1];    // first row of expert e (offsets, held within the activations)
+  int end[kMaxExperts];        // one past its last row
+};
+
+struct Unit {
+  int expert, n0;     // expert; first output column (of N, or of K for the gradient)
+  int m0, m1, width;  // activation rows [m0, m1) of a tile `width` wide
+};
+
+// All threads of the CTA; `ntn`: column tiles per expert.  Ends with a __syncthreads.  Offsets outside 0..m or
+// decreasing (a caller's error) are held to the range, so no tile reaches outside the activations.
+template <int TM>
+__device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restrict__ offsets, int experts, int m,
+                                               int ntn) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int e = tid; e < experts; e += blockDim.x) {
+    int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+    a = a < 0 ? 0 : a > m ? m : a;
+    b = b < a ? a : b > m ? m : b;
+    sc->row[e] = a;
+    sc->end[e] = b;
+  }
+  __syncthreads();
+  if (tid < 32) {  // prefix sum of the experts' units, 32 experts at a time
+    int base = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+      const int e = e0 + lane;
+      int own = e < experts ? (sc->end[e] - sc->row[e] + TM - 1) / TM * ntn : 0;
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
+      }
+      if (e < experts) sc->first[e] = base + sum - own;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) sc->first[experts] = base;
+  }
+  __syncthreads();
+}
+
+// Unit u of the list: experts in order, their column tiles next, row tiles innermost (the row tiles of a column tile
+// run at the same time and share its codes in L2).
+template <int TM>
+__device__ __forceinline__ Unit unit_at(const Schedule* sc, int experts, int u) {
+  int lo = 0, hi = experts;  // first[lo] <= u < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sc->first[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Unit t;
+  t.expert = lo;
+  const int r0 = sc->row[lo], rows = sc->end[lo] - r0;
+  const int ntm = (rows + TM - 1) / TM;
+  const int v = u - sc->first[lo];
+  const int tm = v % ntm;
+  t.n0 = v / ntm * kTileN;
+  t.width = ((rows + ntm - 1) / ntm + 15) & ~15;
+  t.m0 = r0 + tm * t.width;
+  const int m1 = t.m0 + t.width;
+  t.m1 = m1 < sc->end[lo] ? m1 : sc->end[lo];
+  return t;
+}
+
+// `width` activation rows from row m0, 64 columns from x, as boxes of 64 and 16 rows (both whole swizzle atoms)
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map64, const CUtensorMap* map16, int x,
+                                          int m0, int width, uint64_t* bar) {
+  int r = 0;
+  for (; r + 64 <= width; r += 64) tma_load_2d(dst + r * 128, map64, x, m0 + r, bar);
+  for (; r < width; r += 16) tma_load_2d(dst + r * 128, map16, x, m0 + r, bar);
+}
+
+// Accumulator (TMEM lanes = output columns n0 .., columns = rows m0 ..) -> bf16 rows of y, by warps 0..3
+template <class Sm>
+__device__ __forceinline__ void store_unit(const Unit& t, uint32_t taddr, uint16_t* out_stage, Sm* sm,
+                                           uint64_t* acc_empty, __nv_bfloat16* __restrict__ y, int ldy) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t* st = out_stage + warp * (32 * 32);  // this warp's [32 rows][32 columns]
+  const int chunks = (t.width + 31) / 32;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t v[32];
+    tmem_ld32(taddr + c * 32, v);
+    if (c == chunks - 1) {  // read in full: the accumulator may be overwritten
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) st[j * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int piece = lane + 32 * i;  // 128 pieces of 8 bf16
+      const int r = piece >> 2, q = piece & 3;
+      const int m = t.m0 + c * 32 + r;
+      const uint4 o = *reinterpret_cast<const uint4*>(st + r * 32 + q * 8);
+      if (m < t.m1) *reinterpret_cast<uint4*>(y + (int64_t)m * ldy + t.n0 + warp * 32 + q * 8) = o;
+    }
+    __syncwarp();
+  }
+}
+
+}  // namespace experts
+}  // namespace nf4

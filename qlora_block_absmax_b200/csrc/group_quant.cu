@@ -1,0 +1,216 @@
+// group_quant.cu -- weights of uniform 4-bit codes with group scales: quantization and expansion.
+//
+// Quantization of one group of G consecutive columns (G = 32, 64 or 128), every step rounded once in fp32:
+//   with zero points   lo = min(0, min w), hi = max(0, max w), s = T((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15)
+//   symmetric          s = T(max |w| / 7), z = 8
+//   q = clamp(rint(w / s) + z, 0, 15),  rint to the nearest even integer, s == 0: q = z (z = 0 with zero points)
+// where T rounds to the scales' 16-bit type.  Expansion: T'(s (q - z)), the product exact in fp32.
+//
+// One lane holds one packed word (8 codes), G / 8 lanes share a group: a word's source is 16 or 32 contiguous bytes, a
+// warp's stores are 128 contiguous bytes, and a group's range is a shuffle over its lanes.  The division is replaced
+// by a product with 1 / s; a quotient that this leaves within 1e-5 of a rounding border (the product is off by at most
+// 3e-6 for |w / s| <= 16) is divided again, so every code is the one the division gives.  Both kernels are bound by
+// HBM: each weight is read once and written once.
+#include "group.cuh"
+#include "internal.h"
+
+namespace nf4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int kSrc>  // 0 fp32, 1 bf16, 2 fp16
+__device__ __forceinline__ void load8(const void* src, int64_t word, float (&v)[8]) {
+  if constexpr (kSrc == 0) {
+    const float4* p = reinterpret_cast<const float4*>(src) + word * 2;
+    const float4 a = __ldcs(p), b = __ldcs(p + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(src) + word);
+    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = GroupType<kSrc == 2>::to_f32((uint16_t)(r[i] & 0xffffu));
+      v[2 * i + 1] = GroupType<kSrc == 2>::to_f32((uint16_t)(r[i] >> 16));
+    }
+  }
+}
+
+// kL = G / 8 lanes per group; kHalf: fp16 scales (else bf16); kZeros: zero points
+template <int kSrc, int kL, bool kHalf, bool kZeros>
+__global__ void __launch_bounds__(kThreads)
+    quantize_groups_kernel(const void* __restrict__ src, int64_t words, uint32_t* __restrict__ packed,
+                           uint16_t* __restrict__ scale, uint8_t* __restrict__ zero) {
+  using G = GroupType<kHalf>;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  // the loop bound is that of the warp's first lane, so the shuffles always see all 32 lanes; a group lies within
+  // one warp and is present in whole or not at all (words is a multiple of kL)
+  const int lane = threadIdx.x & 31;
+  for (int64_t w0 = (int64_t)blockIdx.x * kThreads + (threadIdx.x - lane); w0 < words; w0 += stride) {
+    const int64_t word = w0 + lane;
+    const bool valid = word < words;
+    float v[8];
+    if (valid) {
+      load8<kSrc>(src, word, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+    float s, z, lo = 0.0f, hi = 0.0f;
+    if constexpr (kZeros) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, v[i]);
+        hi = fmaxf(hi, v[i]);
+      }
+#pragma unroll
+      for (int d = 1; d < kL; d <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi = fmaxf(hi, fabsf(v[i]));
+#pragma unroll
+      for (int d = 1; d < kL; d <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+    }
+    const uint16_t sbits = G::scale_bits(kZeros ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(hi, 7.0f));
+    s = G::to_f32(sbits);
+    z = kZeros ? 0.0f : 8.0f;
+    uint32_t out = 0;
+    if (s > 0.0f) {
+      if constexpr (kZeros) z = fminf(rintf(__fdiv_rn(-lo, s)), 15.0f);
+      const float inv = __fdiv_rn(1.0f, s);
+      float q[8], far = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * inv;
+        q[i] = rintf(t);
+        far = fmaxf(far, fabsf(t - q[i]));
+      }
+      // near a border, or a scale so small that 1 / s is not an ordinary number: divide
+      if (!(far < 0.49999f) || s < 1e-30f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = rintf(__fdiv_rn(v[i], s));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = (uint32_t)fminf(fmaxf(q[i] + z, 0.0f), 15.0f);
+        out |= c << (4 * (i >> 1) + 16 * (i & 1));
+      }
+    } else {
+      out = (uint32_t)z * 0x11111111u;
+    }
+    if (valid) {
+      packed[word] = out;
+      if ((lane & (kL - 1)) == 0) {
+        const int64_t g = word / kL;
+        scale[g] = sbits;
+        if constexpr (kZeros) zero[g] = (uint8_t)z;
+      }
+    }
+  }
+}
+
+// kOut: 0 fp32, 1 bf16, 2 fp16; shift: log2(G / 8), words per group
+template <int kOut, bool kHalf>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_groups_kernel(const uint32_t* __restrict__ packed, const uint16_t* __restrict__ scale,
+                             const uint8_t* __restrict__ zero, int64_t words, int shift, void* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t word = (int64_t)blockIdx.x * kThreads + threadIdx.x; word < words; word += stride) {
+    const uint32_t w = __ldcs(packed + word);
+    const int64_t g = word >> shift;
+    const float s = GroupType<kHalf>::to_f32(__ldg(scale + g));
+    const float z = 8388608.0f + (zero != nullptr ? (float)__ldg(zero + g) : 8.0f);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = (w >> (4 * (i >> 1) + 16 * (i & 1))) & 15u;
+      v[i] = __fmul_rn(__fsub_rn(__uint_as_float(0x4b000000u | c), z), s);  // 2^23 + c, exact
+    }
+    if constexpr (kOut == 0) {
+      float4* p = reinterpret_cast<float4*>(out) + word * 2;
+      __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+    } else {
+      using G = GroupType<kOut == 2>;
+      __stcs(reinterpret_cast<uint4*>(out) + word,
+             make_uint4(G::pack(v[0], v[1]), G::pack(v[2], v[3]), G::pack(v[4], v[5]), G::pack(v[6], v[7])));
+    }
+  }
+}
+
+unsigned grid_for(int64_t words, int num_sms) {
+  const int64_t need = (words + kThreads - 1) / kThreads, most = (int64_t)num_sms * 8;
+  return (unsigned)(need < most ? need : most);
+}
+
+template <int kSrc, int kL, bool kHalf>
+cudaError_t launch_quant(const void* src, int64_t words, const GroupWeight& g, cudaStream_t stream, int num_sms) {
+  auto* packed = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(g.packed));
+  auto* scale = const_cast<uint16_t*>(static_cast<const uint16_t*>(g.scale));
+  auto* zero = const_cast<uint8_t*>(g.zero);
+  const dim3 grid(grid_for(words, num_sms));
+  const cudaError_t e =
+      zero != nullptr ? launch_pdl(quantize_groups_kernel<kSrc, kL, kHalf, true>, grid, dim3(kThreads), 0, stream, src,
+                                   words, packed, scale, zero)
+                      : launch_pdl(quantize_groups_kernel<kSrc, kL, kHalf, false>, grid, dim3(kThreads), 0, stream,
+                                   src, words, packed, scale, zero);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int kSrc, int kL>
+cudaError_t launch_quant_scale(const void* src, int64_t words, const GroupWeight& g, cudaStream_t stream,
+                               int num_sms) {
+  return g.half ? launch_quant<kSrc, kL, true>(src, words, g, stream, num_sms)
+                : launch_quant<kSrc, kL, false>(src, words, g, stream, num_sms);
+}
+
+template <int kSrc>
+cudaError_t launch_quant_group(const void* src, int64_t words, const GroupWeight& g, cudaStream_t stream,
+                               int num_sms) {
+  if (g.group == 32) return launch_quant_scale<kSrc, 4>(src, words, g, stream, num_sms);
+  if (g.group == 64) return launch_quant_scale<kSrc, 8>(src, words, g, stream, num_sms);
+  return launch_quant_scale<kSrc, 16>(src, words, g, stream, num_sms);
+}
+
+template <int kOut>
+cudaError_t launch_dequant(const GroupWeight& g, void* out, cudaStream_t stream, int num_sms) {
+  const int64_t words = g.rows * g.cols / 8;
+  const int shift = g.group == 32 ? 2 : g.group == 64 ? 3 : 4;
+  const auto* packed = reinterpret_cast<const uint32_t*>(g.packed);
+  const auto* scale = static_cast<const uint16_t*>(g.scale);
+  const dim3 grid(grid_for(words, num_sms));
+  const cudaError_t e = g.half ? launch_pdl(dequantize_groups_kernel<kOut, true>, grid, dim3(kThreads), 0, stream,
+                                            packed, scale, g.zero, words, shift, out)
+                               : launch_pdl(dequantize_groups_kernel<kOut, false>, grid, dim3(kThreads), 0, stream,
+                                            packed, scale, g.zero, words, shift, out);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_groups(const void* src, int src_dtype, const GroupWeight& g, cudaStream_t stream,
+                                   int num_sms) {
+  const int64_t words = g.rows * g.cols / 8;
+  if (src_dtype == 0) return launch_quant_group<0>(src, words, g, stream, num_sms);
+  if (src_dtype == 1) return launch_quant_group<1>(src, words, g, stream, num_sms);
+  return launch_quant_group<2>(src, words, g, stream, num_sms);
+}
+
+cudaError_t launch_dequantize_groups(const GroupWeight& g, void* out, int out_dtype, cudaStream_t stream,
+                                     int num_sms) {
+  if (out_dtype == 0) return launch_dequant<0>(g, out, stream, num_sms);
+  if (out_dtype == 1) return launch_dequant<1>(g, out, stream, num_sms);
+  return launch_dequant<2>(g, out, stream, num_sms);
+}
+
+}  // namespace nf4

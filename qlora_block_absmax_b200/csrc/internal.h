@@ -135,6 +135,41 @@ size_t gemm_dx_workspace_bytes(int64_t rows, int64_t cols, int64_t m);
 cudaError_t launch_gemm_dx(const uint8_t* packed, const Scales& s, int64_t rows, int64_t cols, const void* dy,
                            int64_t m, void* dx, void* workspace, unsigned* err, cudaStream_t stream, int num_sms);
 
+// products grouped by expert: rows [offsets[e], offsets[e + 1]) of `in` with expert e's weight, rows
+// [e * rows, (e + 1) * rows) of the stacked weight (rows % 128 == 0, cols % 64 == 0; for the gradient rows % 64 == 0,
+// cols % 128 == 0; experts * rows, cols and m within int32)
+constexpr int kMaxExperts = 256;
+struct ExpertsCall {
+  const uint8_t* packed;
+  Scales scales;
+  int experts;
+  int64_t rows, cols;  // of one expert
+  const int* offsets;  // device, experts + 1
+  const void* in;      // [m, cols], or [m, rows] for the gradient
+  int64_t m;           // >= 1
+  void* out;           // [m, rows], or [m, cols]
+};
+cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
+cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
+
+// a weight of uniform 4-bit codes with group scales (see group.cuh); the quantizer writes through these pointers
+struct GroupWeight {
+  const uint8_t* packed;  // [rows, cols / 2]
+  const void* scale;      // [rows, cols / group] bf16 or fp16
+  const uint8_t* zero;    // [rows, cols / group], or null: 8 everywhere
+  int64_t rows, cols;     // cols a multiple of group
+  int group;              // 32, 64 or 128
+  bool half;              // fp16 scales (else bf16)
+};
+// src_dtype / out_dtype: 0 fp32, 1 bf16, 2 fp16
+cudaError_t launch_quantize_groups(const void* src, int src_dtype, const GroupWeight& g, cudaStream_t stream,
+                                   int num_sms);
+cudaError_t launch_dequantize_groups(const GroupWeight& g, void* out, int out_dtype, cudaStream_t stream,
+                                     int num_sms);
+// x and y of the scales' type, batch 1..8
+cudaError_t launch_gemv_groups(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream,
+                               int num_sms);
+
 // failure-path self-test: a bounded wait that runs out (see selftest.cu)
 cudaError_t launch_wait_timeout(unsigned* err, cudaStream_t stream);
 
