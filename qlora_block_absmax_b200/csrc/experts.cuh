@@ -62,6 +62,15 @@ __device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restri
   __syncthreads();
 }
 
+// One lane of a converged warp.  The MMA warp runs its loop with all lanes and lets one of them issue: the loop's
+// addresses and descriptors then stay in uniform registers, where a loop inside `if (lane == 0)` moves each of them
+// over for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
+}
+
 // Unit u of the list: experts in order, their column tiles next, row tiles innermost (the row tiles of a column tile
 // run at the same time and share its codes in L2).
 template <int TM>

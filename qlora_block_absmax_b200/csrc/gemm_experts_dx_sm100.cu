@@ -41,10 +41,12 @@ constexpr uint32_t kKGroup = 2048;
 template <int TM>
 struct Cfg {
   static constexpr int kStages = TM == 256 ? 4 : 6;    // operand ring: dY tile + decoded tile
-  static constexpr int kWStages = TM == 256 ? 5 : 14;  // packed codes
+  static constexpr int kWStages = TM == 256 ? 4 : 12;  // packed codes
   static constexpr int kBBytes = TM * kTileR * 2;
   static constexpr int kRingBytes = kStages * (kBBytes + kABytes) + kWStages * kWBytes;
   static constexpr int kTmemCols = 2 * TM;  // two accumulators
+  // as in the forward product: the operand ring empties in order, code loads may land out of order
+  static_assert(kStages >= kGroups && kWStages % kGroups == 0, "rings and producer groups");
 };
 
 template <int TM>

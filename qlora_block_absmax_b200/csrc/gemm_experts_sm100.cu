@@ -6,7 +6,7 @@
 // weights, each row going through the expert that its router chose.
 //
 // A work unit is a tile of 128 weight rows (UMMA M) x up to TM activation rows (UMMA N, the tile's own width) over the
-// whole reduction, 64 columns per stage.  The weight tile is decoded by producer warps into TMEM (operand A), the
+// whole reduction, 128 columns (two level-1 blocks per weight row) per stage.  The weight tile is decoded by producer warps into TMEM (operand A), the
 // activation tile comes by TMA (operand B), D[n, t] accumulates in TMEM.  Warp roles of the one persistent CTA per SM:
 //   warps 0-3    epilogue
 //   then 4 G     producers in G groups, each taking every G-th stage: thread p decodes row p of the stage's tile
@@ -24,7 +24,11 @@ namespace {
 
 using namespace experts;
 
-constexpr int kTileK = 64;  // reduction per stage: one level-1 block per weight row
+// Reduction per stage.  The issuing thread pays about 350 cycles per stage for its barrier test, fences and commit
+// besides some 50 per MMA; at 64 columns (four MMAs) that came to 600 cycles per stage, above the time in which the
+// producers decode one.
+constexpr int kTileK = 128;
+constexpr int kHalfK = 64;  // one level-1 block per weight row, one 128-byte swizzle atom of activations
 constexpr int kGroups = 4;
 constexpr int kWBytes = kTileN * kTileK / 2;  // packed codes of a stage
 constexpr int kProdWarp0 = kEpiWarps;
@@ -33,14 +37,22 @@ constexpr int kMmaWarp = kTmaWarp + 1;
 constexpr int kTmaWWarp = kTmaWarp + 2;
 constexpr int kThreads = (kTmaWWarp + 1) * 32;
 
-// TM: widest activation tile, 256, or 64 for few rows per expert (smaller stages leave room for a deeper code ring)
+// TM: widest activation tile, 128, or 64 for few rows per expert (smaller stages leave room for a deeper code ring)
 template <int TM>
 struct Cfg {
-  static constexpr int kStages = TM == 256 ? 5 : 8;    // operand ring: activation tile + 32 TMEM columns of weights
-  static constexpr int kWStages = TM == 256 ? 8 : 24;  // packed codes
-  static constexpr int kBBytes = TM * kTileK * 2;
+  static constexpr int kStages = TM == 128 ? 4 : 6;    // operand ring: activation tile + 64 TMEM columns of weights
+  static constexpr int kWStages = TM == 128 ? 8 : 12;  // packed codes
+  static constexpr int kAccs = 2;                      // accumulators: an epilogue runs beside the next tile
+  static constexpr int kHalfB = TM * kHalfK * 2;
+  static constexpr int kBBytes = 2 * kHalfB;
   static constexpr int kRingBytes = kStages * kBBytes + kWStages * kWBytes;
-  static constexpr int kTmemCols = TM + kStages * 32 <= 256 ? 256 : 512;
+  static constexpr int kACol0 = kAccs * TM;  // first TMEM column of the decoded tiles
+  static constexpr int kTmemCols = 512;
+  static_assert(kACol0 + kStages * kTileK / 2 <= kTmemCols, "TMEM columns");
+  // A parity wait tells two successive phases of a barrier apart, no more.  A group comes back to a ring kGroups
+  // stages later: it must not reach a slot whose phase before the awaited one is still open.  The operand ring empties
+  // in order, so kGroups stages suffice; code loads may land out of order, so each slot belongs to one group.
+  static_assert(kStages >= kGroups && kWStages % kGroups == 0, "rings and producer groups");
 };
 
 template <int TM>
@@ -49,7 +61,7 @@ struct Smem {
   uint64_t wempty[Cfg<TM>::kWStages];
   uint64_t full[Cfg<TM>::kStages];
   uint64_t empty[Cfg<TM>::kStages];
-  uint64_t acc_full, acc_empty;
+  uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
   float unit_lut[256];
@@ -60,7 +72,7 @@ template <int TM>
 constexpr size_t smem_bytes() {
   return (size_t)Cfg<TM>::kRingBytes + kEpiWarps * kStageOutBytes + sizeof(Smem<TM>) + 1024;
 }
-static_assert(smem_bytes<256>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
 
 template <bool kDQ, int kBook, int TM>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -89,8 +101,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->full[i], 1 + 4);
       mbar_init(&sm->empty[i], 1);
     }
-    mbar_init(&sm->acc_full, 1);
-    mbar_init(&sm->acc_empty, kEpiWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->acc_full[i], 1);
+      mbar_init(&sm->acc_empty[i], kEpiWarps);
+    }
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -107,7 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int units = sm->sc.first[experts], kps = cols / kTileK;
+  const int units = sm->sc.first[experts], kps = (cols + kTileK - 1) / kTileK;
+  const bool odd = cols % kTileK != 0;  // the last stage holds one block
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
     // ------------------------------------------------ producers
@@ -117,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const DecodeMul dm = decode_mul();
     uint32_t it = group;
     int u = blockIdx.x, ks = group;
+    const int rb = cols / kBlock;
     int64_t block0 = 0;  // level-1 block of this thread's row at column 0
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
       while (ks >= kps && u < units) {
@@ -125,50 +141,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (u < units) {
         const Unit t = unit_at<TM>(&sm->sc, experts, u);
-        block0 = ((int64_t)t.expert * rows + t.n0 + p) * kps;
+        block0 = ((int64_t)t.expert * rows + t.n0 + p) * rb;
       }
     };
     settle();
-    uint32_t code = 0;  // the stage's scale, loaded one of this group's stages ahead
-    float scale = 0.0f;
+    uint32_t code[2] = {0, 0};  // the stage's scales, loaded one of this group's stages ahead
+    float scale[2] = {0.0f, 0.0f};
     auto load_scale = [&]() {
       if (u >= units) return;
-      const int64_t b = block0 + ks;
-      if (kDQ) {
-        code = __ldg(s.q + b);
-        scale = __ldg(s.scale + b / kDqBlock);
-      } else {
-        scale = __ldg(s.absmax + b);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && 2 * ks + 1 >= rb) break;
+        const int64_t b = block0 + 2 * ks + h;
+        if (kDQ) {
+          code[h] = __ldg(s.q + b);
+          scale[h] = __ldg(s.scale + b / kDqBlock);
+        } else {
+          scale[h] = __ldg(s.absmax + b);
+        }
       }
     };
     load_scale();
-    while (u < units) {
+    bool ok = true;
+    while (u < units && ok) {
       const int ws = it % kWStages, as = it % kStages;
       const uint32_t wph = (it / kWStages) & 1, aph = (it / kStages) & 1;
-      const float a = kDQ ? dq_absmax(sm->unit_lut[code], scale, mu) : scale;
+      float a[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a[h] = kDQ ? dq_absmax(sm->unit_lut[code[h]], scale[h], mu) : scale[h];
+      const int blocks = 2 * ks + 1 < rb ? 2 : 1;
       ks += kGroups;
       if (ks >= kps) settle();
       load_scale();
-      if (!wait_or_abort(&sm->wfull[ws], wph, sm, err)) break;
-      const uint4* wsrc = reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + p * 32);
-      const uint4 w0 = wsrc[0], w1 = wsrc[1];
-      fence_proxy_async_smem();  // the slot is refilled by TMA after these reads
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->wempty[ws]);
-      const Table T = make_table<kBook>(a);
-      const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      uint32_t r[32];  // column j of the row: codes 2j, 2j + 1 as bf16x2
+      ok = wait_or_abort(&sm->wfull[ws], wph, sm, err);
+      if (!ok) break;
+      const uint4* wsrc = reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + p * (kTileK / 2));
+      const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(C::kACol0 + as * (kTileK / 2));
+#pragma unroll 1
+      for (int h = 0; h < blocks; ++h) {
+        // 64-byte swizzle: 16-byte piece c of row p lies at piece c ^ ((p / 2) % 4)
+        const uint4 w0 = wsrc[(2 * h) ^ ((p >> 1) & 3)], w1 = wsrc[(2 * h + 1) ^ ((p >> 1) & 3)];
+        if (h == blocks - 1) {
+          fence_proxy_async_smem();  // the slot is refilled by TMA after these reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->wempty[ws]);
+        }
+        const Table T = make_table<kBook>(h == 0 ? a[0] : a[1]);
+        const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t r[32];  // column j of the row: codes 2j, 2j + 1 as bf16x2
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t d[4];
-        decode_word(words[c], T, d, dm);
-        r[4 * c] = d[0];
-        r[4 * c + 1] = d[1];
-        r[4 * c + 2] = d[2];
-        r[4 * c + 3] = d[3];
+        for (int c = 0; c < 8; ++c) {
+          uint32_t d[4];
+          decode_word(words[c], T, d, dm);
+          r[4 * c] = d[0];
+          r[4 * c + 1] = d[1];
+          r[4 * c + 2] = d[2];
+          r[4 * c + 3] = d[3];
+        }
+        if (h == 0) ok = wait_or_abort(&sm->empty[as], aph ^ 1, sm, err);  // the MMAs left this slot
+        if (!ok) break;
+        tmem_st32(ta + h * (kHalfK / 2), r);
       }
-      if (!wait_or_abort(&sm->empty[as], aph ^ 1, sm, err)) break;  // the MMAs left this slot
-      tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(TM + as * 32), r);
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->full[as]);
@@ -185,8 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
           if (!ok) break;
-          mbar_expect_tx(&sm->full[as], (uint32_t)t.width * kTileK * 2);
-          load_rows(b_smem0 + as * C::kBBytes, &xmap64, &xmap16, ks * kTileK, t.m0, t.width, &sm->full[as]);
+          const int halves = odd && ks == kps - 1 ? 1 : 2;
+          mbar_expect_tx(&sm->full[as], (uint32_t)(t.width * halves) * kHalfK * 2);
+          for (int h = 0; h < halves; ++h)
+            load_rows(b_smem0 + as * C::kBBytes + h * C::kHalfB, &xmap64, &xmap16, ks * kTileK + h * kHalfK, t.m0,
+                      t.width, &sm->full[as]);
         }
       }
       for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)  // drain the copies still in flight
@@ -213,36 +250,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t it = 0, ucount = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++ucount) {
-        const uint32_t idesc = instr_desc(kTileN, unit_at<TM>(&sm->sc, experts, u).width);
-        ok = wait_or_abort(&sm->acc_empty, (ucount & 1) ^ 1, sm, err);
+    const uint32_t tm_u = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t bdesc0 = smem_desc_sw128(b_smem0);
+    uint32_t as = 0, ph = 0, ucount = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++ucount) {
+      const uint32_t idesc = instr_desc(kTileN, __shfl_sync(0xffffffffu, unit_at<TM>(&sm->sc, experts, u).width, 0));
+      const uint32_t acc = ucount % C::kAccs;
+      ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d_tm = tm_u + acc * TM;
+      for (int ks = 0; ks < kps; ++ks) {
+        ok = wait_or_abort(&sm->full[as], ph, sm, err);
         if (!ok) break;
         tc_fence_after();
-        for (int ks = 0; ks < kps; ++ks, ++it) {
-          const int as = it % kStages;
-          ok = wait_or_abort(&sm->full[as], (it / kStages) & 1, sm, err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a_tm = tmem + (uint32_t)(TM + as * 32), b_addr = b_smem0 + as * C::kBBytes;
+        const uint32_t a_tm = tm_u + C::kACol0 + as * (kTileK / 2);
+        const uint64_t bdesc = bdesc0 + as * (C::kBBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk)
-            tc_mma_ts(tmem, a_tm + kk * 8, smem_desc_sw128(b_addr + kk * 32), idesc, (ks | kk) != 0);
+          for (int kk = 0; kk < kHalfK / 16; ++kk)
+            tc_mma_ts(d_tm, a_tm + kk * 8, bdesc + kk * 2, idesc, (ks | kk) != 0);
+          if (!odd || ks < kps - 1) {
+#pragma unroll
+            for (int kk = 0; kk < kHalfK / 16; ++kk)
+              tc_mma_ts(d_tm, a_tm + kHalfK / 2 + kk * 8, bdesc + (C::kHalfB >> 4) + kk * 2, idesc, 1);
+          }
           tc_commit(&sm->empty[as]);
         }
-        if (ok) tc_commit(&sm->acc_full);
+        __syncwarp();
+        if (++as == kStages) {
+          as = 0;
+          ph ^= 1;
+        }
       }
+      if (ok && elect_one()) tc_commit(&sm->acc_full[acc]);
+      __syncwarp();
     }
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++ucount) {
       const Unit t = unit_at<TM>(&sm->sc, experts, u);
-      if (!wait_or_abort(&sm->acc_full, ucount & 1, sm, err)) break;
+      const uint32_t acc = ucount % C::kAccs;
+      if (!wait_or_abort(&sm->acc_full[acc], (ucount / C::kAccs) & 1, sm, err)) break;
       tc_fence_after();
-      store_unit(t, tmem + ((uint32_t)(warp * 32) << 16), out_stage, sm, &sm->acc_empty, y, rows);
+      store_unit(t, tmem + ((uint32_t)(warp * 32) << 16) + acc * TM, out_stage, sm, &sm->acc_empty[acc], y, rows);
     }
   }
 
@@ -289,18 +342,18 @@ cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& x64, const CUte
 
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
   CUtensorMap x64, x16, wmap;
-  if (!make_map(&x64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kTileK, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&x16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kTileK, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!make_map(&x64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&x16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.packed, c.cols / 2, c.rows * c.experts, kTileK / 2, kTileN,
-                CU_TENSOR_MAP_SWIZZLE_NONE))
+                CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorNotSupported;
   // no more units than the row tiles that m rows can make, each with all column tiles
   const bool wide = c.m > 64 * (int64_t)c.experts;
-  const int64_t tm = wide ? 256 : 64;
+  const int64_t tm = wide ? 128 : 64;
   const int64_t tiles = (c.m < c.experts ? c.m : c.experts) + c.m / tm;
   const int64_t units = tiles * (c.rows / kTileN);
   const int grid = (int)(units < num_sms ? units : num_sms);
-  return wide ? launch_form<256>(c, x64, x16, wmap, grid, err, stream)
+  return wide ? launch_form<128>(c, x64, x16, wmap, grid, err, stream)
               : launch_form<64>(c, x64, x16, wmap, grid, err, stream);
 }
 
