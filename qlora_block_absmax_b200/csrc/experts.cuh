@@ -62,6 +62,61 @@ __device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restri
   __syncthreads();
 }
 
+// Decode through a shared table of fp32 code pairs: entry v (a byte of two codes) at 256 v, sixteen copies of 8 bytes,
+// lane l reading copy l % 16, so each half-warp phase of a 64-bit load meets every bank once.  The table is 64 KB-aligned:
+// one byte permute of the packed word with the lane's offset and the table's upper address bytes is the address.  A pair
+// costs that permute, one load, one packed multiply and one convert -- 16 instructions per word of 8 codes, 8 of them on
+// the ALU pipe, where the byte-permute decode (nf4_decode.cuh) takes 21 and 19 and a table of 16 products per block; the
+// price is 8 shared-memory wavefronts per word and warp.  The values are the same: bf16_rn(RN(code * a)).
+constexpr uint32_t kPairTable = 65536;  // bytes and alignment (the second half of every 256 bytes stays unused)
+
+__constant__ float c_code_experts[2][16] = {NF4_CODE_INIT, FP4_CODE_INIT};  // by code book
+
+template <int kBook>
+__device__ __forceinline__ void fill_pair_table(uint8_t* table) {
+  for (int i = threadIdx.x; i < 256 * 8; i += blockDim.x) {  // two copies of an entry
+    const int v = i >> 3;
+    const float hi = c_code_experts[kBook][v >> 4], lo = c_code_experts[kBook][v & 15];
+    *reinterpret_cast<float4*>(table + v * 256 + (i & 7) * 16) = make_float4(hi, lo, hi, lo);
+  }
+}
+
+// byte 0: 8 * (lane % 16), byte 1: 0, bytes 2-3: the upper half of the table's shared address
+__device__ __forceinline__ uint32_t pair_lane(uint32_t table) { return table | (uint32_t)((threadIdx.x & 15) * 8); }
+
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t addr, uint64_t aa) {
+  uint32_t d;
+  asm("{\n .reg .b64 c;\n .reg .f32 x, y;\n ld.shared.b64 c, [%1];\n mul.rn.f32x2 c, c, %2;\n"
+      " mov.b64 {x, y}, c;\n cvt.rn.bf16x2.f32 %0, y, x;\n}"
+      : "=r"(d)
+      : "r"(addr), "l"(aa));
+  return d;
+}
+
+// 8 codes of a packed word -> out[b] = (code 2b, code 2b + 1) * a
+__device__ __forceinline__ void decode_word_pairs(uint32_t w, uint32_t lane_base, uint64_t aa, uint32_t* out) {
+  out[0] = scaled_pair(prmt(w, lane_base, 0x7604u), aa);
+  out[1] = scaled_pair(prmt(w, lane_base, 0x7614u), aa);
+  out[2] = scaled_pair(prmt(w, lane_base, 0x7624u), aa);
+  out[3] = scaled_pair(prmt(w, lane_base, 0x7634u), aa);
+}
+
+__device__ __forceinline__ uint64_t both(float a) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(a));
+  return d;
+}
+
+// 32 lanes x 16 consecutive 32-bit columns from registers; st_wait before they are read
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // One lane of a converged warp.  The MMA warp runs its loop with all lanes and lets one of them issue: the loop's
 // addresses and descriptors then stay in uniform registers, where a loop inside `if (lane == 0)` moves each of them
 // over for every instruction.

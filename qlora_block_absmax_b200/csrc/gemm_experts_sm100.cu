@@ -29,7 +29,8 @@ using namespace experts;
 // producers decode one.
 constexpr int kTileK = 128;
 constexpr int kHalfK = 64;  // one level-1 block per weight row, one 128-byte swizzle atom of activations
-constexpr int kGroups = 4;
+constexpr int kGroups = 4;         // two per stage, one for each of its blocks
+constexpr int kLanes = kGroups / 2;  // stages being decoded at a time
 constexpr int kWBytes = kTileN * kTileK / 2;  // packed codes of a stage
 constexpr int kProdWarp0 = kEpiWarps;
 constexpr int kTmaWarp = kProdWarp0 + 4 * kGroups;
@@ -40,19 +41,18 @@ constexpr int kThreads = (kTmaWWarp + 1) * 32;
 // TM: widest activation tile, 128, or 64 for few rows per expert (smaller stages leave room for a deeper code ring)
 template <int TM>
 struct Cfg {
-  static constexpr int kStages = TM == 128 ? 4 : 6;    // operand ring: activation tile + 64 TMEM columns of weights
-  static constexpr int kWStages = TM == 128 ? 8 : 12;  // packed codes
+  static constexpr int kStages = TM == 128 ? 3 : 6;    // operand ring: activation tile + 64 TMEM columns of weights
+  static constexpr int kWStages = 6;                    // packed codes
   static constexpr int kAccs = 2;                      // accumulators: an epilogue runs beside the next tile
   static constexpr int kHalfB = TM * kHalfK * 2;
   static constexpr int kBBytes = 2 * kHalfB;
-  static constexpr int kRingBytes = kStages * kBBytes + kWStages * kWBytes;
   static constexpr int kACol0 = kAccs * TM;  // first TMEM column of the decoded tiles
   static constexpr int kTmemCols = 512;
   static_assert(kACol0 + kStages * kTileK / 2 <= kTmemCols, "TMEM columns");
-  // A parity wait tells two successive phases of a barrier apart, no more.  A group comes back to a ring kGroups
+  // A parity wait tells two successive phases of a barrier apart, no more.  A group comes back to a ring kLanes
   // stages later: it must not reach a slot whose phase before the awaited one is still open.  The operand ring empties
-  // in order, so kGroups stages suffice; code loads may land out of order, so each slot belongs to one group.
-  static_assert(kStages >= kGroups && kWStages % kGroups == 0, "rings and producer groups");
+  // in order, so kLanes stages suffice; code loads may land out of order, so each slot belongs to one pair of groups.
+  static_assert(kStages >= kLanes && kWStages % kLanes == 0, "rings and producer groups");
 };
 
 template <int TM>
@@ -68,11 +68,19 @@ struct Smem {
   Schedule sc;
 };
 
+// Shared memory: the packed codes, the epilogue's staging and Smem before the pair table at 64 KB, the activation ring
+// after it.  The window of a CTA without static shared memory starts at 1 KB (the kernel checks that all of it fits).
+constexpr uint32_t kWindow = 1024;
 template <int TM>
 constexpr size_t smem_bytes() {
-  return (size_t)Cfg<TM>::kRingBytes + kEpiWarps * kStageOutBytes + sizeof(Smem<TM>) + 1024;
+  return 2 * (size_t)kPairTable - kWindow + Cfg<TM>::kStages * Cfg<TM>::kBBytes;
+}
+template <int TM>
+constexpr uint32_t front_bytes() {
+  return Cfg<TM>::kWStages * kWBytes + kEpiWarps * kStageOutBytes + (uint32_t)sizeof(Smem<TM>);
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
+static_assert(kWindow + front_bytes<128>() <= kPairTable && kWindow + front_bytes<64>() <= kPairTable, "front part");
 
 template <bool kDQ, int kBook, int TM>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -84,21 +92,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t b_smem0 = base, w_smem0 = base + kStages * C::kBBytes;
-  const uint8_t* w_gen0 = gbase + kStages * C::kBBytes;
-  uint16_t* out_stage = reinterpret_cast<uint16_t*>(gbase + C::kRingBytes);
-  auto* sm = reinterpret_cast<Smem<TM>*>(gbase + C::kRingBytes + kEpiWarps * kStageOutBytes);
+  const uint32_t front = (raw + 1023u) & ~1023u, table = kPairTable;
+  uint8_t* w_gen0 = smem_raw + (front - raw);
+  const uint32_t w_smem0 = front, b_smem0 = table + kPairTable;
+  uint16_t* out_stage = reinterpret_cast<uint16_t*>(w_gen0 + kWStages * kWBytes);
+  auto* sm = reinterpret_cast<Smem<TM>*>(w_gen0 + kWStages * kWBytes + kEpiWarps * kStageOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (front != kWindow) {  // the window does not start at 1 KB: refuse, touch nothing
+    if (threadIdx.x == 0) atomicOr(err, kErrTimeout);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWStages; ++i) {
       mbar_init(&sm->wfull[i], 1);
-      mbar_init(&sm->wempty[i], 4);
+      mbar_init(&sm->wempty[i], 8);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm->full[i], 1 + 4);
+      mbar_init(&sm->full[i], 1 + 8);
       mbar_init(&sm->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -115,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  fill_pair_table<kBook>(smem_raw + (table - raw));
   pdl_wait();
   build_schedule<TM>(&sm->sc, offsets, experts, m_total, rows / kTileN);
   tc_fence_before();
@@ -126,14 +138,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
     // ------------------------------------------------ producers
-    const int group = (warp - kProdWarp0) >> 2;
-    const int p = ((warp - kProdWarp0) & 3) * 32 + lane;  // weight row within the tile
+    const int group = (warp - kProdWarp0) >> 2, h = group & 1;  // h: this group's block of the stage
+    const int p = ((warp - kProdWarp0) & 3) * 32 + lane;        // weight row within the tile
     const float mu = kDQ ? __ldg(s.mean) : 0.0f;
-    const DecodeMul dm = decode_mul();
-    uint32_t it = group;
-    int u = blockIdx.x, ks = group;
+    const uint32_t lane_base = pair_lane(table);
+    const uint32_t ta0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(C::kACol0 + h * (kHalfK / 2));
     const int rb = cols / kBlock;
-    int64_t block0 = 0;  // level-1 block of this thread's row at column 0
+    // the stage whose scale is loaded next: unit, stage of the unit, and where its scales lie
+    int u = blockIdx.x, ks = group >> 1;
+    const uint8_t* q_row = nullptr;    // scale codes (double quant) of this thread's row from its block h on,
+    const float* s_row = nullptr;      // the second-level scale of the row's first block and
+    uint32_t s_off = 0;                // that block's place among the 256; or (plain) the row's scales
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
       while (ks >= kps && u < units) {
         ks -= kps;
@@ -141,72 +156,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (u < units) {
         const Unit t = unit_at<TM>(&sm->sc, experts, u);
-        block0 = ((int64_t)t.expert * rows + t.n0 + p) * rb;
-      }
-    };
-    settle();
-    uint32_t code[2] = {0, 0};  // the stage's scales, loaded one of this group's stages ahead
-    float scale[2] = {0.0f, 0.0f};
-    auto load_scale = [&]() {
-      if (u >= units) return;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && 2 * ks + 1 >= rb) break;
-        const int64_t b = block0 + 2 * ks + h;
+        const int64_t b = ((int64_t)t.expert * rows + t.n0 + p) * rb + h;
         if (kDQ) {
-          code[h] = __ldg(s.q + b);
-          scale[h] = __ldg(s.scale + b / kDqBlock);
+          q_row = s.q + b;
+          s_row = s.scale + b / kDqBlock;
+          s_off = (uint32_t)(b % kDqBlock);
         } else {
-          scale[h] = __ldg(s.absmax + b);
+          s_row = s.absmax + b;
         }
       }
     };
-    load_scale();
-    bool ok = true;
-    while (u < units && ok) {
-      const int ws = it % kWStages, as = it % kStages;
-      const uint32_t wph = (it / kWStages) & 1, aph = (it / kStages) & 1;
-      float a[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) a[h] = kDQ ? dq_absmax(sm->unit_lut[code[h]], scale[h], mu) : scale[h];
-      const int blocks = 2 * ks + 1 < rb ? 2 : 1;
-      ks += kGroups;
-      if (ks >= kps) settle();
-      load_scale();
-      ok = wait_or_abort(&sm->wfull[ws], wph, sm, err);
-      if (!ok) break;
-      const uint4* wsrc = reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + p * (kTileK / 2));
-      const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(C::kACol0 + as * (kTileK / 2));
-#pragma unroll 1
-      for (int h = 0; h < blocks; ++h) {
-        // 64-byte swizzle: 16-byte piece c of row p lies at piece c ^ ((p / 2) % 4)
-        const uint4 w0 = wsrc[(2 * h) ^ ((p >> 1) & 3)], w1 = wsrc[(2 * h + 1) ^ ((p >> 1) & 3)];
-        if (h == blocks - 1) {
-          fence_proxy_async_smem();  // the slot is refilled by TMA after these reads
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->wempty[ws]);
-        }
-        const Table T = make_table<kBook>(h == 0 ? a[0] : a[1]);
-        const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        uint32_t r[32];  // column j of the row: codes 2j, 2j + 1 as bf16x2
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t d[4];
-          decode_word(words[c], T, d, dm);
-          r[4 * c] = d[0];
-          r[4 * c + 1] = d[1];
-          r[4 * c + 2] = d[2];
-          r[4 * c + 3] = d[3];
-        }
-        if (h == 0) ok = wait_or_abort(&sm->empty[as], aph ^ 1, sm, err);  // the MMAs left this slot
-        if (!ok) break;
-        tmem_st32(ta + h * (kHalfK / 2), r);
+    uint32_t code = 0;
+    float scale = 0.0f;
+    auto load_scale = [&]() {  // of block 2 ks + h; the second block of an odd reduction's last stage does not exist
+      if (u >= units || 2 * ks + h >= rb) return;
+      if (kDQ) {
+        code = __ldg(q_row + 2 * ks);
+        scale = __ldg(s_row + ((s_off + 2 * ks) / kDqBlock));
+      } else {
+        scale = __ldg(s_row + 2 * ks);
       }
-      if (!ok) break;
+    };
+    uint32_t ws = group >> 1, wph = 0, as = group >> 1, aph = 1;
+    // codes of the next stage: 64-byte swizzle, 16-byte piece c of row p lies at piece c ^ ((p / 2) % 4)
+    const uint32_t c0 = (uint32_t)(p * (kTileK / 2) + (((2 * h) ^ ((p >> 1) & 3)) << 4));
+    uint4 n0, n1;
+    auto load_codes = [&]() -> bool {
+      if (!wait_or_abort(&sm->wfull[ws], wph, sm, err)) return false;
+      n0 = *reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + c0);
+      n1 = *reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + (c0 ^ 16u));
+      fence_proxy_async_smem();  // the slot is refilled by TMA after these reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->wempty[ws]);
+      ws += kLanes;
+      if (ws >= kWStages) {
+        ws -= kWStages;
+        wph ^= 1;
+      }
+      return true;
+    };
+    // software pipeline: while a stage is decoded, the codes of the group's next stage are on their way from shared
+    // memory and the scale after that from global memory
+    settle();
+    load_scale();
+    bool more = u < units;
+    if (more) more = load_codes();
+    while (more) {
+      const uint64_t aa = both(kDQ ? dq_absmax(sm->unit_lut[code], scale, mu) : scale);
+      const bool some = 2 * ks + h < rb;
+      const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+      ks += kLanes;
+      if (ks >= kps) settle();
+      more = u < units;
+      load_scale();
+      if (more) more = load_codes();
+      const uint32_t ta = ta0 + as * (kTileK / 2);  // column j: codes 2j, 2j + 1 of the block as bf16x2
+      uint32_t r[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) decode_word_pairs(words[c], lane_base, aa, r + 4 * c);
+      if (!wait_or_abort(&sm->empty[as], aph, sm, err)) break;  // the MMAs left this slot
+      if (some) tmem_st16(ta, r);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) decode_word_pairs(words[4 + c], lane_base, aa, r + 4 * c);
+      if (some) tmem_st16(ta + 16, r);
+      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->full[as]);
-      it += kGroups;
+      as += kLanes;
+      if (as >= kStages) {
+        as -= kStages;
+        aph ^= 1;
+      }
     }
   } else if (warp == kTmaWarp) {
     // ------------------------------------------------ TMA: activation tiles
