@@ -144,11 +144,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = pair_lane(table);
     const uint32_t ta0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(C::kACol0 + h * (kHalfK / 2));
     const int rb = cols / kBlock;
-    // the stage whose scale is loaded next: unit, stage of the unit, and where its scales lie
-    int u = blockIdx.x, ks = group >> 1;
-    const uint8_t* q_row = nullptr;    // scale codes (double quant) of this thread's row from its block h on,
-    const float* s_row = nullptr;      // the second-level scale of the row's first block and
-    uint32_t s_off = 0;                // that block's place among the 256; or (plain) the row's scales
+    // Scales of this thread's row, from its block h of the unit's first stage on; the group's blocks are 2 kLanes
+    // apart.  A warp's rows lie in 32 different cache lines, so each load instruction costs as many lookups: the scale
+    // codes come 16 at a time where rows of codes are 16-byte aligned (`vec`), a second-level scale only when the row
+    // enters another block of 256.
+    int u = blockIdx.x, ks = group >> 1;  // the stage whose scale is loaded next
+    const uint8_t* q_row = nullptr;       // (double quant) codes; s_row: second-level scale of the row's first block,
+    const float* s_row = nullptr;         // s_off: that block's place among the 256; (plain) the row's scales
+    uint32_t s_off = 0, s_at = ~0u;       // s_at: the second-level scale held
+    const bool vec = kDQ && rb % 16 == 0 && (reinterpret_cast<uintptr_t>(s.q) & 15) == 0;
+    uint4 chunk = make_uint4(0, 0, 0, 0);
+    uint32_t code = 0;
+    float scale = 0.0f;
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
       while (ks >= kps && u < units) {
         ks -= kps;
@@ -156,35 +163,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (u < units) {
         const Unit t = unit_at<TM>(&sm->sc, experts, u);
-        const int64_t b = ((int64_t)t.expert * rows + t.n0 + p) * rb + h;
+        const int64_t b = ((int64_t)t.expert * rows + t.n0 + p) * rb;
         if (kDQ) {
           q_row = s.q + b;
           s_row = s.scale + b / kDqBlock;
           s_off = (uint32_t)(b % kDqBlock);
+          s_at = ~0u;
+          if (vec) chunk = __ldg(reinterpret_cast<const uint4*>(q_row) + 2 * ks / 16);
         } else {
           s_row = s.absmax + b;
         }
       }
     };
-    uint32_t code = 0;
-    float scale = 0.0f;
     auto load_scale = [&]() {  // of block 2 ks + h; the second block of an odd reduction's last stage does not exist
-      if (u >= units || 2 * ks + h >= rb) return;
+      const int b = 2 * ks + h;
+      if (u >= units || b >= rb) return;
       if (kDQ) {
-        code = __ldg(q_row + 2 * ks);
-        scale = __ldg(s_row + ((s_off + 2 * ks) / kDqBlock));
+        if (vec) {
+          if (b % 16 < 2 * kLanes) chunk = __ldg(reinterpret_cast<const uint4*>(q_row + (b & ~15)));
+        } else {
+          code = __ldg(q_row + b);
+        }
+        const uint32_t at = (s_off + b) / kDqBlock;
+        if (at != s_at) {
+          s_at = at;
+          scale = __ldg(s_row + at);
+        }
       } else {
-        scale = __ldg(s_row + 2 * ks);
+        scale = __ldg(s_row + b);
       }
     };
+    // the block that load_scale went to last: its code's value in [-1, 1] (double quant), and from it its scale
+    auto block_unit = [&]() -> float {
+      if (!kDQ) return 0.0f;
+      if (vec) {
+        const uint32_t b = (uint32_t)(2 * ks + h);
+        const uint32_t lo = b & 4 ? chunk.y : chunk.x, hi = b & 4 ? chunk.w : chunk.z;
+        code = ((b & 8 ? hi : lo) >> (8 * (b & 3))) & 0xffu;
+      }
+      return sm->unit_lut[code];
+    };
+    auto block_scale = [&](float unit) -> uint64_t { return both(kDQ ? dq_absmax(unit, scale, mu) : scale); };
     uint32_t ws = group >> 1, wph = 0, as = group >> 1, aph = 1;
-    // codes of the next stage: 64-byte swizzle, 16-byte piece c of row p lies at piece c ^ ((p / 2) % 4)
+    // codes of a stage: 64-byte swizzle, 16-byte piece c of row p lies at piece c ^ ((p / 2) % 4)
     const uint32_t c0 = (uint32_t)(p * (kTileK / 2) + (((2 * h) ^ ((p >> 1) & 3)) << 4));
     uint4 n0, n1;
     auto load_codes = [&]() -> bool {
       if (!wait_or_abort(&sm->wfull[ws], wph, sm, err)) return false;
       n0 = *reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + c0);
       n1 = *reinterpret_cast<const uint4*>(w_gen0 + ws * kWBytes + (c0 ^ 16u));
+      return true;
+    };
+    auto release_codes = [&]() {
       fence_proxy_async_smem();  // the slot is refilled by TMA after these reads
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->wempty[ws]);
@@ -193,16 +223,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ws -= kWStages;
         wph ^= 1;
       }
-      return true;
     };
-    // software pipeline: while a stage is decoded, the codes of the group's next stage are on their way from shared
-    // memory and the scale after that from global memory
+    // Software pipeline.  The shared-memory pipe is the busiest, and a load queues behind the table lookups of all
+    // sixteen warps; so the codes and the scale of the group's next stage are read while this one is decoded, and only
+    // the two halves' lookups wait for their own round.
     settle();
     load_scale();
     bool more = u < units;
-    if (more) more = load_codes();
+    uint64_t aa = 0;
+    if (more) {
+      aa = block_scale(block_unit());
+      more = load_codes();
+      if (more) release_codes();
+    }
     while (more) {
-      const uint64_t aa = both(kDQ ? dq_absmax(sm->unit_lut[code], scale, mu) : scale);
       const bool some = 2 * ks + h < rb;
       const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
       ks += kLanes;
@@ -214,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t r[16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) decode_word_pairs(words[c], lane_base, aa, r + 4 * c);
+      const float unit = block_unit();
+      if (more) release_codes();
       if (!wait_or_abort(&sm->empty[as], aph, sm, err)) break;  // the MMAs left this slot
       if (some) tmem_st16(ta, r);
 #pragma unroll
@@ -228,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         as -= kStages;
         aph ^= 1;
       }
+      aa = block_scale(unit);
     }
   } else if (warp == kTmaWarp) {
     // ------------------------------------------------ TMA: activation tiles
