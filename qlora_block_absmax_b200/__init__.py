@@ -57,15 +57,24 @@ def _need_cuda(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _on_device(device: torch.device):
-    """The CUDA device of the tensors as the current one (a no-op when it already is)."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+_SAME_DEVICE = contextlib.nullcontext()
 
 
-def _need_out(out: torch.Tensor, shape, dtype: torch.dtype, device: torch.device) -> None:
+def _on_device(t: torch.Tensor):
+    """The tensor's CUDA device as the current one (a no-op when it already is)."""
+    return _SAME_DEVICE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.get_device())
+
+
+def _raw_stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
+    """The handle of `stream`, or of the current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _need_out(out: torch.Tensor, shape, like: torch.Tensor, dtype: Optional[torch.dtype] = None) -> None:
     _need_cuda(out, "out")
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
-        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    dtype = like.dtype if dtype is None else dtype
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != like.get_device():
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {like.device}")
 
 
 @dataclass
@@ -371,37 +380,44 @@ def gemm_dx_workspace_bytes(qw: QuantizedWeight, m: int) -> int:
     return int(_lib.load().nf4_gemm_dx_workspace_bytes(ctypes.byref(d), m))
 
 
-def _experts(name: str, qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int, gradient: bool,
-             out, workspace, stream) -> torch.Tensor:
-    for t, what in ((x, "dy" if gradient else "x"), (offsets, "offsets")):
-        _need_cuda(t, what)
-        if t.device != qw.packed.device:
-            raise ValueError(f"{what} must be on the weight's device")
-    if x.dtype != torch.bfloat16:
+def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int,
+             width: int, owidth: int, out, workspace, stream) -> torch.Tensor:
+    packed = qw.packed
+    if not (x.is_cuda and offsets.is_cuda and x.get_device() == offsets.get_device() == packed.get_device()):
+        raise ValueError("activations and offsets must be CUDA tensors on the weight's device")
+    if not (x.is_contiguous() and offsets.is_contiguous()):
+        raise ValueError("activations and offsets must be contiguous")
+    if x.dtype is not torch.bfloat16:
         raise TypeError("activations must be bfloat16")
-    if offsets.dtype != torch.int32 or offsets.numel() != experts + 1:
+    if offsets.dtype is not torch.int32 or offsets.numel() != experts + 1:
         raise ValueError("offsets must be int32 with experts + 1 entries")
-    if experts < 1 or qw.rows % experts:
-        raise ValueError("the weight's rows must be a multiple of experts")
-    n = qw.rows // experts
-    width, owidth = (n, qw.cols) if gradient else (qw.cols, n)
     if x.dim() < 1 or x.shape[-1] != width:
         raise ValueError(f"the activations' last dimension must be {width}")
     m = x.numel() // width if width else 0
-    with _on_device(x.device):
-        lib = _lib.load()
-        d = qw.descriptor()
+    with _on_device(x):
+        d = ctypes.byref(qw.descriptor())
         if out is None:
-            out = torch.empty(m, owidth, dtype=torch.bfloat16, device=x.device)
+            out = x.new_empty((m, owidth))
         else:
-            _need_out(out, (m, owidth), torch.bfloat16, x.device)
-        ws_bytes = getattr(lib, name + "_workspace_bytes")(ctypes.byref(d), experts, m)
-        if workspace is None and ws_bytes:
-            workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=x.device)  # zeroed once, then reusable
-        st = getattr(lib, name)(ctypes.byref(d), experts, _ptr(x), _ptr(offsets), m, _ptr(out), _ptr(workspace),
-                                workspace.numel() if workspace is not None else 0, _stream(stream))
-        _lib.check(st, name)
+            _need_out(out, (m, owidth), x)
+        if workspace is None:
+            ws_bytes = size(d, experts, m)
+            if ws_bytes:
+                workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=x.device)  # zeroed once, then reusable
+        elif not workspace.is_cuda or workspace.get_device() != x.get_device():
+            raise ValueError("workspace must be on the weight's device")
+        st = call(d, experts, x.data_ptr(), offsets.data_ptr(), m, out.data_ptr(),
+                  workspace.data_ptr() if workspace is not None else None,
+                  workspace.numel() * workspace.element_size() if workspace is not None else 0, _raw_stream(x, stream))
+        if st:
+            _lib.check(st, what)
     return out
+
+
+def _expert_rows(qw: QuantizedWeight, experts: int) -> int:
+    if experts < 1 or qw.rows % experts:
+        raise ValueError("the weight's rows must be a multiple of experts")
+    return qw.rows // experts
 
 
 def gemm_experts(qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int, out=None,
@@ -411,7 +427,9 @@ def gemm_experts(qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, ex
 
     qw stacks the experts' weights (rows = experts * N); x is bf16 [m, cols], sorted by expert; offsets is int32
     [experts + 1] on the GPU.  Rows that no expert has are left unwritten (undefined in a fresh output)."""
-    return _experts("nf4_gemm_experts", qw, x, offsets, experts, False, out, workspace, stream)
+    lib = _lib.load()
+    return _experts(lib.nf4_gemm_experts, lib.nf4_gemm_experts_workspace_bytes, "nf4_gemm_experts", qw, x, offsets,
+                    experts, qw.cols, _expert_rows(qw, experts), out, workspace, stream)
 
 
 def gemm_experts_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
@@ -423,7 +441,9 @@ def gemm_experts_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> i
 def gemm_experts_dx(qw: QuantizedWeight, dy: torch.Tensor, offsets: torch.Tensor, experts: int, out=None,
                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Input gradient of ``gemm_experts``: dX[t] = bf16(Wc_e^T dY[t]) for dY bf16 [m, N] sorted by expert."""
-    return _experts("nf4_gemm_experts_dx", qw, dy, offsets, experts, True, out, workspace, stream)
+    lib = _lib.load()
+    return _experts(lib.nf4_gemm_experts_dx, lib.nf4_gemm_experts_dx_workspace_bytes, "nf4_gemm_experts_dx", qw, dy,
+                    offsets, experts, _expert_rows(qw, experts), qw.cols, out, workspace, stream)
 
 
 def gemm_experts_dx_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
@@ -449,23 +469,21 @@ class GroupWeight:
     group: int = 128
 
     def descriptor(self) -> _lib.NF4GroupWeight:
-        if self.scale.dtype not in (torch.bfloat16, torch.float16):
+        packed, scale, zero, rows, cols, group = self.packed, self.scale, self.zero, self.rows, self.cols, self.group
+        code = _FLOAT_CODES.get(scale.dtype)
+        if code not in (NF4_BF16, NF4_F16):
             raise TypeError("scale must be bfloat16 or float16")
-        groups = self.rows * (self.cols // self.group) if self.group > 0 else 0
-        for t, name, n in ((self.packed, "packed", self.rows * self.cols // 2), (self.scale, "scale", groups),
-                           (self.zero, "zero", groups)):
-            if t is None:
-                continue
-            _need_cuda(t, name)
-            if t.device != self.packed.device:
-                raise ValueError(f"{name} must be on the weight's device")
-            if t.numel() != n:
-                raise ValueError(f"{name} must have {n} entries")
-        for t, name in ((self.packed, "packed"), (self.zero, "zero")):
-            if t is not None and t.dtype != torch.uint8:
-                raise TypeError(f"{name} must be uint8")
-        return _lib.NF4GroupWeight(_ptr(self.packed), _ptr(self.scale), _ptr(self.zero), self.rows, self.cols,
-                                   self.group, _FLOAT_CODES[self.scale.dtype])
+        if packed.dtype is not torch.uint8 or (zero is not None and zero.dtype is not torch.uint8):
+            raise TypeError("packed and zero must be uint8")
+        n = rows * (cols // group) if group > 0 else 0
+        dev = packed.get_device()
+        if not (packed.is_cuda and packed.is_contiguous() and packed.numel() == rows * cols // 2):
+            raise ValueError(f"packed must be a contiguous CUDA tensor of {rows * cols // 2} bytes")
+        for t in (scale,) if zero is None else (scale, zero):
+            if not (t.is_contiguous() and t.get_device() == dev and t.numel() == n):
+                raise ValueError(f"scale and zero must be contiguous, of {n} entries and on the codes' device")
+        return _lib.NF4GroupWeight(packed.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
+                                   rows, cols, group, code)
 
 
 def quantize_groups(w: torch.Tensor, group: int = 128, symmetric: bool = False,
@@ -485,14 +503,15 @@ def quantize_groups(w: torch.Tensor, group: int = 128, symmetric: bool = False,
     rows, cols = w.shape
     if group not in (32, 64, 128) or cols % group:
         raise ValueError("group must be 32, 64 or 128 and divide cols")
-    with _on_device(w.device):
-        packed = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
-        scale = torch.empty(rows, cols // group, dtype=scale_dtype, device=w.device)
-        zero = None if symmetric else torch.empty(rows, cols // group, dtype=torch.uint8, device=w.device)
-        st = _lib.load().nf4_quantize_groups(_ptr(w), _FLOAT_CODES[w.dtype], rows, cols, group,
-                                             _FLOAT_CODES[scale_dtype], _ptr(packed), _ptr(scale), _ptr(zero),
-                                             _stream(stream))
-        _lib.check(st, "nf4_quantize_groups")
+    with _on_device(w):
+        packed = w.new_empty((rows, cols // 2), dtype=torch.uint8)
+        scale = w.new_empty((rows, cols // group), dtype=scale_dtype)
+        zero = None if symmetric else w.new_empty((rows, cols // group), dtype=torch.uint8)
+        st = _lib.load().nf4_quantize_groups(w.data_ptr(), _FLOAT_CODES[w.dtype], rows, cols, group,
+                                             _FLOAT_CODES[scale_dtype], packed.data_ptr(), scale.data_ptr(),
+                                             None if symmetric else zero.data_ptr(), _raw_stream(w, stream))
+        if st:
+            _lib.check(st, "nf4_quantize_groups")
     return GroupWeight(packed=packed, scale=scale, zero=zero, rows=rows, cols=cols, group=group)
 
 
@@ -501,35 +520,38 @@ def dequantize_groups(gw: GroupWeight, dtype: torch.dtype = torch.float32, out=N
     if dtype not in _FLOAT_CODES:
         raise TypeError("dequantize_groups produces float32, bfloat16 or float16")
     d = gw.descriptor()
-    with _on_device(gw.packed.device):
+    with _on_device(gw.packed):
         if out is None:
-            out = torch.empty(gw.rows, gw.cols, dtype=dtype, device=gw.packed.device)
+            out = gw.packed.new_empty((gw.rows, gw.cols), dtype=dtype)
         else:
-            _need_out(out, (gw.rows, gw.cols), dtype, gw.packed.device)
-        st = _lib.load().nf4_dequantize_groups(ctypes.byref(d), _ptr(out), _FLOAT_CODES[dtype], _stream(stream))
-        _lib.check(st, "nf4_dequantize_groups")
+            _need_out(out, (gw.rows, gw.cols), gw.packed, dtype)
+        st = _lib.load().nf4_dequantize_groups(ctypes.byref(d), out.data_ptr(), _FLOAT_CODES[dtype],
+                                               _raw_stream(out, stream))
+        if st:
+            _lib.check(st, "nf4_dequantize_groups")
     return out
 
 
 def gemv_groups(gw: GroupWeight, x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """y[b, n] = sum_k scale * (code - zero) * x[b, k] for x [B, cols] of the scales' type, 1 <= B <= 8; fp32 sums,
     the weight not rounded to 16 bits."""
-    _need_cuda(x, "x")
-    if x.dtype != gw.scale.dtype:
+    if not (x.is_cuda and x.is_contiguous() and x.get_device() == gw.packed.get_device()):
+        raise ValueError("x must be a contiguous CUDA tensor on the weight's device")
+    if x.dtype is not gw.scale.dtype:
         raise TypeError("x must have the scales' type")
-    if x.device != gw.packed.device:
-        raise ValueError("x must be on the weight's device")
-    if x.dim() < 1 or x.shape[-1] != gw.cols:
+    cols, rows = gw.cols, gw.rows
+    if x.dim() < 1 or x.shape[-1] != cols:
         raise ValueError("x must have cols columns")
     d = gw.descriptor()
-    batch = x.numel() // gw.cols if gw.cols else x.shape[:-1].numel()
-    with _on_device(x.device):
+    batch = x.numel() // cols if cols else x.shape[:-1].numel()
+    with _on_device(x):
         if out is None:
-            out = torch.empty(batch, gw.rows, dtype=x.dtype, device=x.device)
+            out = x.new_empty((batch, rows))
         else:
-            _need_out(out, (batch, gw.rows), x.dtype, x.device)
-        st = _lib.load().nf4_gemv_groups(ctypes.byref(d), _ptr(x), batch, _ptr(out), _stream(stream))
-        _lib.check(st, "nf4_gemv_groups")
+            _need_out(out, (batch, rows), x)
+        st = _lib.load().nf4_gemv_groups(ctypes.byref(d), x.data_ptr(), batch, out.data_ptr(), _raw_stream(x, stream))
+        if st:
+            _lib.check(st, "nf4_gemv_groups")
     return out
 
 

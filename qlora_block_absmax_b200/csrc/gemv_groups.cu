@@ -10,6 +10,10 @@
 // group of 128 each lane takes four consecutive words of the step, at 64 two and two, at 32 single words four apart.
 // The order of k inside an MMA is free as long as both operands use the same one: a word's pairs (0,1), (2,3) feed one
 // MMA and (4,5), (6,7) the next, against 16 contiguous bytes of x.
+//
+// The kernel lives on bytes in flight: each warp keeps kDepth steps of codes (1 KB each) loading in registers, and the
+// scales of the tile's 16 rows -- contiguous in memory -- come as one coalesced copy into shared memory, already
+// widened to (fp32 scale, packed bias + zero point), 256 groups at a time.
 // The warps' sums are added in a fixed order, so results are deterministic.
 #include "group.cuh"
 #include "internal.h"
@@ -17,8 +21,10 @@
 namespace nf4 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStep = 128;  // columns per warp step
+constexpr int kWarps = 8;
+constexpr int kDepth = 4;
+constexpr int kStep = 128;    // columns per warp step
+constexpr int kChunk = 256;   // groups of scales in shared memory at a time
 
 // word of slot i (0..3) and lane t within a step, by group size
 template <int kGroup>
@@ -26,42 +32,30 @@ __device__ __forceinline__ int slot_word(int i, int t) {
   return kGroup == 128 ? 4 * t + i : kGroup == 64 ? 8 * (i >> 1) + 2 * t + (i & 1) : 4 * i + t;
 }
 
+// codes of rows g and g + 8; `left`: columns from the step's first one to the row's end
 template <int kGroup>
-struct Step {
-  static constexpr int kSub = kStep / kGroup;  // groups per step
-  uint32_t w[2][4];       // words of rows g, g + 8
-  uint16_t s[2][kSub];    // scales
-  uint8_t z[2][kSub];     // zero points
-};
-
-template <int kGroup, bool kZeros>
-__device__ __forceinline__ void load_step(Step<kGroup>& d, const uint8_t* __restrict__ packed,
-                                          const uint16_t* __restrict__ scale, const uint8_t* __restrict__ zero,
-                                          const int64_t (&row)[2], int64_t cols, int64_t st, int t) {
-  constexpr int kSub = Step<kGroup>::kSub;
-  const int64_t groups = cols / kGroup;
+__device__ __forceinline__ void load_step(uint32_t (&w)[2][4], const uint8_t* __restrict__ p0,
+                                          const uint8_t* __restrict__ p1, int64_t left, int t) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint8_t* p = packed + row[h] * (cols / 2) + st * (kStep / 2);
+    const uint8_t* p = h ? p1 : p0;
+    if constexpr (kGroup == 128) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + t);
+      w[h][0] = v.x;
+      w[h][1] = v.y;
+      w[h][2] = v.z;
+      w[h][3] = v.w;
+    } else if constexpr (kGroup == 64) {
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) {
-      const bool ok = st * kSub + j < groups;  // the last step may be short by whole groups
-      if constexpr (kGroup == 128) {
-        const uint4 v = ok ? __ldcs(reinterpret_cast<const uint4*>(p) + t) : make_uint4(0, 0, 0, 0);
-        d.w[h][0] = v.x;
-        d.w[h][1] = v.y;
-        d.w[h][2] = v.z;
-        d.w[h][3] = v.w;
-      } else if constexpr (kGroup == 64) {
-        const uint2 v = ok ? __ldcs(reinterpret_cast<const uint2*>(p) + 4 * j + t) : make_uint2(0, 0);
-        d.w[h][2 * j] = v.x;
-        d.w[h][2 * j + 1] = v.y;
-      } else {
-        d.w[h][j] = ok ? __ldcs(reinterpret_cast<const uint32_t*>(p) + 4 * j + t) : 0u;
+      for (int j = 0; j < 2; ++j) {
+        const uint2 v = 64 * j < left ? __ldcs(reinterpret_cast<const uint2*>(p) + 4 * j + t) : make_uint2(0, 0);
+        w[h][2 * j] = v.x;
+        w[h][2 * j + 1] = v.y;
       }
-      const int64_t gi = row[h] * groups + st * kSub + j;
-      d.s[h][j] = ok ? __ldg(scale + gi) : (uint16_t)0;
-      d.z[h][j] = kZeros && ok ? __ldg(zero + gi) : (uint8_t)8;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[h][j] = 32 * j < left ? __ldcs(reinterpret_cast<const uint32_t*>(p) + 4 * j + t) : 0u;
     }
   }
 }
@@ -70,50 +64,82 @@ template <bool kHalf, int kGroup, bool kZeros>
 __global__ void __launch_bounds__(kWarps * 32)
     gemv_groups_kernel(const uint8_t* __restrict__ packed, const uint16_t* __restrict__ scale,
                        const uint8_t* __restrict__ zero, int64_t rows, int64_t cols, const uint16_t* __restrict__ x,
-                       int batch, uint16_t* __restrict__ y) {
+                       int batch, uint16_t* __restrict__ y, int pitch) {
   using G = GroupType<kHalf>;
-  constexpr int kSub = Step<kGroup>::kSub, kSlots = 4 / kSub;  // word slots per group
+  constexpr int kSub = kStep / kGroup, kSlots = 4 / kSub;  // groups per step, word slots per group
   __shared__ float red[kWarps][16][8];
+  extern __shared__ float2 meta[];  // [16][pitch]: fp32 scale, packed bias + zero point
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int64_t r0 = (int64_t)blockIdx.x * 16 + g;
+  const int64_t tile = (int64_t)blockIdx.x * 16;
+  const int64_t r0 = tile + g;
   // rows past the last one read it again; they are not written
-  const int64_t row[2] = {r0 < rows ? r0 : rows - 1, r0 + 8 < rows ? r0 + 8 : rows - 1};
-  const int64_t nsteps = (cols + kStep - 1) / kStep;
+  const int64_t ra = r0 < rows ? r0 : rows - 1, rb = r0 + 8 < rows ? r0 + 8 : rows - 1;
+  const int groups = (int)(cols / kGroup), nsteps = (groups + kSub - 1) / kSub;
+  const int mine = warp < nsteps ? (nsteps - warp + kWarps - 1) / kWarps : 0;  // steps of this warp
+  const uint8_t* p0 = packed + ra * (cols / 2) + warp * (kStep / 2);
+  const uint8_t* p1 = packed + rb * (cols / 2) + warp * (kStep / 2);
   const uint16_t* xr = x + (int64_t)g * cols;
+  const bool has = g < batch;
+  uint32_t buf[kDepth][2][4];
+  auto load = [&](int i, uint32_t (&w)[2][4]) {
+    const int64_t off = (int64_t)i * (kWarps * kStep / 2);
+    load_step<kGroup>(w, p0 + off, p1 + off, cols - ((int64_t)i * kWarps + warp) * kStep, t);
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (d < mine) load(d, buf[d]);
+
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  Step<kGroup> cur, nxt;
-  if (warp < nsteps) load_step<kGroup, kZeros>(cur, packed, scale, zero, row, cols, warp, t);
-  for (int64_t st = warp; st < nsteps; st += kWarps) {
-    if (st + kWarps < nsteps) load_step<kGroup, kZeros>(nxt, packed, scale, zero, row, cols, st + kWarps, t);
-#pragma unroll
-    for (int j = 0; j < kSub; ++j) {
-      const uint32_t z0 = G::pack(G::kBiasF + (float)cur.z[0][j], G::kBiasF + (float)cur.z[0][j]);
-      const uint32_t z1 = G::pack(G::kBiasF + (float)cur.z[1][j], G::kBiasF + (float)cur.z[1][j]);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = j * kSlots; i < (j + 1) * kSlots; ++i) {
-        const int64_t k = st * kStep + 8 * slot_word<kGroup>(i, t);
-        uint4 xv = make_uint4(0, 0, 0, 0);
-        if (g < batch && k < cols) xv = __ldg(reinterpret_cast<const uint4*>(xr + k));
-        uint32_t a[2][4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          a[0][p] = G::sub2(((cur.w[0][i] >> (4 * p)) & 0x000f000fu) | G::kBias, z0);
-          a[1][p] = G::sub2(((cur.w[1][i] >> (4 * p)) & 0x000f000fu) | G::kBias, z1);
-        }
-        G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y);
-        G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w);
-      }
-      const float s0 = G::to_f32(cur.s[0][j]), s1 = G::to_f32(cur.s[1][j]);
-      acc[0] = fmaf(s0, part[0], acc[0]);
-      acc[1] = fmaf(s0, part[1], acc[1]);
-      acc[2] = fmaf(s1, part[2], acc[2]);
-      acc[3] = fmaf(s1, part[3], acc[3]);
+  constexpr int kPerChunk = kChunk / kSub / kWarps;  // steps per warp and chunk
+  static_assert(kPerChunk % kDepth == 0, "chunks hold whole rounds");
+  for (int c = 0; c * kChunk < groups; ++c) {
+    const int gn = groups - c * kChunk < kChunk ? groups - c * kChunk : kChunk;
+    if (c > 0) __syncthreads();
+    for (int i = threadIdx.x; i < 16 * gn; i += kWarps * 32) {
+      const int r = i / gn, j = i - r * gn;
+      const int64_t at = (tile + r < rows ? tile + r : rows - 1) * groups + c * kChunk + j;
+      const float z = G::kBiasF + (kZeros ? (float)__ldg(zero + at) : 8.0f);
+      meta[r * pitch + j] = make_float2(G::to_f32(__ldg(scale + at)), __uint_as_float(G::pack(z, z)));
     }
-    cur = nxt;
+    __syncthreads();
+    const int end = (c + 1) * kPerChunk < mine ? (c + 1) * kPerChunk : mine;
+    for (int i0 = c * kPerChunk; i0 < end; i0 += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int i = i0 + d;
+        if (i >= end) break;
+        const int64_t k0 = ((int64_t)i * kWarps + warp) * kStep;
+        const int j0 = (i * kWarps + warp) * kSub - c * kChunk;  // first group of the step within the chunk
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+          if (kGroup < 128 && j0 + j >= gn) break;  // the last step may be short by whole groups
+          const float2 m0 = meta[g * pitch + j0 + j], m1 = meta[(g + 8) * pitch + j0 + j];
+          const uint32_t z0 = __float_as_uint(m0.y), z1 = __float_as_uint(m1.y);
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = j * kSlots; s < (j + 1) * kSlots; ++s) {
+            uint4 xv = make_uint4(0, 0, 0, 0);
+            if (has) xv = __ldg(reinterpret_cast<const uint4*>(xr + k0 + 8 * slot_word<kGroup>(s, t)));
+            uint32_t a[2][4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              a[0][p] = G::sub2(((buf[d][0][s] >> (4 * p)) & 0x000f000fu) | G::kBias, z0);
+              a[1][p] = G::sub2(((buf[d][1][s] >> (4 * p)) & 0x000f000fu) | G::kBias, z1);
+            }
+            G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y);
+            G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w);
+          }
+          acc[0] = fmaf(m0.x, part[0], acc[0]);
+          acc[1] = fmaf(m0.x, part[1], acc[1]);
+          acc[2] = fmaf(m1.x, part[2], acc[2]);
+          acc[3] = fmaf(m1.x, part[3], acc[3]);
+        }
+        if (i + kDepth < mine) load(i + kDepth, buf[d]);
+      }
+    }
   }
   // accumulator fragment: (row g, batch 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
   red[warp][g][2 * t] = acc[0];
@@ -122,15 +148,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   red[warp][g + 8][2 * t + 1] = acc[3];
   __syncthreads();
   const int r = threadIdx.x & 15, b = threadIdx.x >> 4;
-  const int64_t n = (int64_t)blockIdx.x * 16 + r;
-  if (b < batch && n < rows) {
+  if (b < batch && tile + r < rows) {
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += red[w][r][b];
-    y[(int64_t)b * rows + n] = (uint16_t)(G::pack(sum, 0.0f) & 0xffffu);
+    y[(int64_t)b * rows + tile + r] = (uint16_t)(G::pack(sum, 0.0f) & 0xffffu);
   }
 }
-static_assert(kWarps * 32 == 16 * 8, "one thread per output of the tile");
+static_assert(kWarps * 32 >= 16 * 8, "a thread per output of the tile");
 
 template <bool kHalf, int kGroup>
 cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream) {
@@ -138,11 +163,15 @@ cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cuda
   const auto* scale = static_cast<const uint16_t*>(w.scale);
   const auto* xs = static_cast<const uint16_t*>(x);
   auto* ys = static_cast<uint16_t*>(y);
+  const int64_t groups = w.cols / kGroup;
+  // an odd pitch spreads the eight rows that a warp reads at once over the banks
+  const int pitch = (int)(groups < kChunk ? groups : kChunk) | 1;
+  const size_t smem = (size_t)16 * pitch * sizeof(float2);
   const cudaError_t e =
-      w.zero != nullptr ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true>, grid, block, 0, stream, w.packed, scale,
-                                     w.zero, w.rows, w.cols, xs, batch, ys)
-                        : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false>, grid, block, 0, stream, w.packed, scale,
-                                     w.zero, w.rows, w.cols, xs, batch, ys);
+      w.zero != nullptr ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true>, grid, block, smem, stream, w.packed,
+                                     scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch)
+                        : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false>, grid, block, smem, stream, w.packed,
+                                     scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
