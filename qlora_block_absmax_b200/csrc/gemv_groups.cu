@@ -21,10 +21,15 @@
 namespace nf4 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kDepth = 4;
 constexpr int kStep = 128;    // columns per warp step
 constexpr int kChunk = 256;   // groups of scales in shared memory at a time
+
+// (v & 0x000f000f) | bias in one LOP3
+__device__ __forceinline__ uint32_t nibbles_or(uint32_t v, uint32_t bias) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(d) : "r"(v), "r"(bias));
+  return d;
+}
 
 // word of slot i (0..3) and lane t within a step, by group size
 template <int kGroup>
@@ -35,7 +40,7 @@ __device__ __forceinline__ int slot_word(int i, int t) {
 // codes of rows g and g + 8; `left`: columns from the step's first one to the row's end
 template <int kGroup>
 __device__ __forceinline__ void load_step(uint32_t (&w)[2][4], const uint8_t* __restrict__ p0,
-                                          const uint8_t* __restrict__ p1, int64_t left, int t) {
+                                          const uint8_t* __restrict__ p1, int left, int t) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint8_t* p = h ? p1 : p0;
@@ -60,7 +65,7 @@ __device__ __forceinline__ void load_step(uint32_t (&w)[2][4], const uint8_t* __
   }
 }
 
-template <bool kHalf, int kGroup, bool kZeros>
+template <bool kHalf, int kGroup, bool kZeros, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32)
     gemv_groups_kernel(const uint8_t* __restrict__ packed, const uint16_t* __restrict__ scale,
                        const uint8_t* __restrict__ zero, int64_t rows, int64_t cols, const uint16_t* __restrict__ x,
@@ -71,6 +76,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   extern __shared__ float2 meta[];  // [16][pitch]: fp32 scale, packed bias + zero point
   pdl_launch_dependents();
   pdl_wait();
+  uint32_t bias;  // kept in a register: as a constant beside the mask it would cost a second instruction per use
+  asm volatile("mov.b32 %0, %1;" : "=r"(bias) : "n"(G::kBias));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int64_t tile = (int64_t)blockIdx.x * 16;
@@ -78,15 +85,18 @@ __global__ void __launch_bounds__(kWarps * 32)
   // rows past the last one read it again; they are not written
   const int64_t ra = r0 < rows ? r0 : rows - 1, rb = r0 + 8 < rows ? r0 + 8 : rows - 1;
   const int groups = (int)(cols / kGroup), nsteps = (groups + kSub - 1) / kSub;
-  const int mine = warp < nsteps ? (nsteps - warp + kWarps - 1) / kWarps : 0;  // steps of this warp
-  const uint8_t* p0 = packed + ra * (cols / 2) + warp * (kStep / 2);
-  const uint8_t* p1 = packed + rb * (cols / 2) + warp * (kStep / 2);
-  const uint16_t* xr = x + (int64_t)g * cols;
-  const bool has = g < batch;
+  // a warp takes two neighbouring steps at a time (128 bytes of a row, a whole cache line), the warps in turn
+  auto step_of = [&](int i) { return ((i >> 1) * kWarps + warp) * 2 + (i & 1); };
+  const int full = nsteps / (2 * kWarps), rest = nsteps - full * 2 * kWarps - 2 * warp;
+  const int mine = 2 * full + (rest <= 0 ? 0 : rest == 1 ? 1 : 2);  // steps of this warp
+  const uint8_t* p0 = packed + ra * (cols / 2);
+  const uint8_t* p1 = packed + rb * (cols / 2);
+  // lanes past the batch read its last row again: their columns of the product are not written
+  const uint16_t* xr = x + (int64_t)(g < batch ? g : batch - 1) * cols + 8 * slot_word<kGroup>(0, t);
   uint32_t buf[kDepth][2][4];
   auto load = [&](int i, uint32_t (&w)[2][4]) {
-    const int64_t off = (int64_t)i * (kWarps * kStep / 2);
-    load_step<kGroup>(w, p0 + off, p1 + off, cols - ((int64_t)i * kWarps + warp) * kStep, t);
+    const int st = step_of(i), off = st * (kStep / 2);
+    load_step<kGroup>(w, p0 + off, p1 + off, (int)cols - st * kStep, t);
   };
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
@@ -94,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   constexpr int kPerChunk = kChunk / kSub / kWarps;  // steps per warp and chunk
-  static_assert(kPerChunk % kDepth == 0, "chunks hold whole rounds");
+  static_assert(kPerChunk % kDepth == 0 && kPerChunk % 2 == 0 && kPerChunk > 0, "chunks hold whole rounds");
   for (int c = 0; c * kChunk < groups; ++c) {
     const int gn = groups - c * kChunk < kChunk ? groups - c * kChunk : kChunk;
     if (c > 0) __syncthreads();
@@ -111,26 +121,29 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int d = 0; d < kDepth; ++d) {
         const int i = i0 + d;
         if (i >= end) break;
-        const int64_t k0 = ((int64_t)i * kWarps + warp) * kStep;
-        const int j0 = (i * kWarps + warp) * kSub - c * kChunk;  // first group of the step within the chunk
+        const int k0 = step_of(i) * kStep;
+        const int j0 = step_of(i) * kSub - c * kChunk;  // first group of the step within the chunk
 #pragma unroll
         for (int j = 0; j < kSub; ++j) {
           if (kGroup < 128 && j0 + j >= gn) break;  // the last step may be short by whole groups
           const float2 m0 = meta[g * pitch + j0 + j], m1 = meta[(g + 8) * pitch + j0 + j];
           const uint32_t z0 = __float_as_uint(m0.y), z1 = __float_as_uint(m1.y);
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          float part[4];
 #pragma unroll
           for (int s = j * kSlots; s < (j + 1) * kSlots; ++s) {
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            if (has) xv = __ldg(reinterpret_cast<const uint4*>(xr + k0 + 8 * slot_word<kGroup>(s, t)));
+            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + k0 + 8 * (slot_word<kGroup>(s, 0))));
             uint32_t a[2][4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              a[0][p] = G::sub2(((buf[d][0][s] >> (4 * p)) & 0x000f000fu) | G::kBias, z0);
-              a[1][p] = G::sub2(((buf[d][1][s] >> (4 * p)) & 0x000f000fu) | G::kBias, z1);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w = buf[d][h][s], z = h ? z1 : z0;
+#pragma unroll
+              for (int p = 0; p < 4; ++p) a[h][p] = G::sub2(nibbles_or(w >> (4 * p), bias), z);
             }
-            G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y);
-            G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w);
+            if (s == j * kSlots)
+              G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+            else
+              G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, part[0], part[1], part[2], part[3]);
+            G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w, part[0], part[1], part[2], part[3]);
           }
           acc[0] = fmaf(m0.x, part[0], acc[0]);
           acc[1] = fmaf(m0.x, part[1], acc[1]);
@@ -155,10 +168,10 @@ __global__ void __launch_bounds__(kWarps * 32)
     y[(int64_t)b * rows + tile + r] = (uint16_t)(G::pack(sum, 0.0f) & 0xffffu);
   }
 }
-static_assert(kWarps * 32 >= 16 * 8, "a thread per output of the tile");
 
-template <bool kHalf, int kGroup>
-cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream) {
+template <bool kHalf, int kGroup, int kWarps, int kDepth>
+cudaError_t launch_shape(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream) {
+  static_assert(kWarps * 32 >= 16 * 8, "a thread per output of the tile");
   const dim3 grid((unsigned)((w.rows + 15) / 16)), block(kWarps * 32);
   const auto* scale = static_cast<const uint16_t*>(w.scale);
   const auto* xs = static_cast<const uint16_t*>(x);
@@ -168,28 +181,39 @@ cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cuda
   const int pitch = (int)(groups < kChunk ? groups : kChunk) | 1;
   const size_t smem = (size_t)16 * pitch * sizeof(float2);
   const cudaError_t e =
-      w.zero != nullptr ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true>, grid, block, smem, stream, w.packed,
-                                     scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch)
-                        : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false>, grid, block, smem, stream, w.packed,
-                                     scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch);
+      w.zero != nullptr
+          ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true, kWarps, kDepth>, grid, block, smem, stream, w.packed,
+                       scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch)
+          : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false, kWarps, kDepth>, grid, block, smem, stream, w.packed,
+                       scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <bool kHalf, int kGroup>
+cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream, int num_sms) {
+  // Few tiles: sixteen warps share a tile's columns (4096x14336 batch 1: 11.6 us against 14.0 with eight).  Many: eight,
+  // so that more tiles are under way on an SM (14336x4096 batch 1: 12.6 us against 13.8, batch 8 in groups of 64: 15.9
+  // against 18.2).
+  return (w.rows + 15) / 16 <= 2 * (int64_t)num_sms ? launch_shape<kHalf, kGroup, 16, 2>(w, x, batch, y, stream)
+                                                    : launch_shape<kHalf, kGroup, 8, 2>(w, x, batch, y, stream);
+}
+
 template <bool kHalf>
-cudaError_t launch_group_size(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream) {
-  if (w.group == 32) return launch<kHalf, 32>(w, x, batch, y, stream);
-  if (w.group == 64) return launch<kHalf, 64>(w, x, batch, y, stream);
-  return launch<kHalf, 128>(w, x, batch, y, stream);
+cudaError_t launch_group_size(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream,
+                              int num_sms) {
+  if (w.group == 32) return launch<kHalf, 32>(w, x, batch, y, stream, num_sms);
+  if (w.group == 64) return launch<kHalf, 64>(w, x, batch, y, stream, num_sms);
+  return launch<kHalf, 128>(w, x, batch, y, stream, num_sms);
 }
 
 }  // namespace
 
 cudaError_t launch_gemv_groups(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream,
                                int num_sms) {
-  (void)num_sms;
   if ((w.rows + 15) / 16 > INT32_MAX) return cudaErrorInvalidValue;
-  return w.half ? launch_group_size<true>(w, x, batch, y, stream) : launch_group_size<false>(w, x, batch, y, stream);
+  return w.half ? launch_group_size<true>(w, x, batch, y, stream, num_sms)
+                : launch_group_size<false>(w, x, batch, y, stream, num_sms);
 }
 
 }  // namespace nf4
