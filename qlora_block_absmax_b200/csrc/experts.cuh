@@ -126,9 +126,9 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Unit u of the list: experts in order, their column tiles next, row tiles innermost (the row tiles of a column tile
-// run at the same time and share its codes in L2).
-template <int TM>
+// Unit u of the list: experts in order, their column tiles (kCols wide) next, row tiles innermost (the row tiles of a
+// column tile run at the same time and share its codes in L2).
+template <int TM, int kCols = kTileN>
 __device__ __forceinline__ Unit unit_at(const Schedule* sc, int experts, int u) {
   int lo = 0, hi = experts;  // first[lo] <= u < first[hi]
   while (hi - lo > 1) {
@@ -144,12 +144,102 @@ __device__ __forceinline__ Unit unit_at(const Schedule* sc, int experts, int u) 
   const int ntm = (rows + TM - 1) / TM;
   const int v = u - sc->first[lo];
   const int tm = v % ntm;
-  t.n0 = v / ntm * kTileN;
-  t.width = ((rows + ntm - 1) / ntm + 15) & ~15;
+  t.n0 = v / ntm * kCols;
+  constexpr int kAlign = kCols / kTileN * 16;  // each CTA of a pair loads half the tile, in boxes of 16 rows
+  t.width = ((rows + ntm - 1) / ntm + kAlign - 1) & ~(kAlign - 1);
   t.m0 = r0 + tm * t.width;
   const int m1 = t.m0 + t.width;
   t.m1 = m1 < sc->end[lo] ? m1 : sc->end[lo];
   return t;
+}
+
+// ------------------------------------------------------------------ CTA pairs (cta_group::2)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// arrive at CTA 0's barrier of the same name
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// wait_or_abort for a barrier that the other CTA arrives at
+template <class Sm>
+__device__ __forceinline__ bool wait_or_abort_cluster(uint64_t* bar, uint32_t parity, Sm* sm, unsigned* err) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (aborted(sm)) return false;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) break;
+  }
+  atomicOr(err, kErrTimeout);
+  *(volatile int*)&sm->abort = 1;
+  return false;
+}
+
+// D (TMEM of both CTAs, 128 rows each) (+)= A (TMEM of both) . B (half of its rows in each CTA's shared memory)
+__device__ __forceinline__ void tc_mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// arrive at the barrier of both CTAs once the MMAs issued so far have finished
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n"
+                 "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)),
+                 "r"(cols)
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n"
+                 "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::"r"(smem_u32(dst)),
+                 "r"(cols)
+                 : "memory");
+  }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
 // `width` activation rows from row m0, 64 columns from x, as boxes of 64 and 16 rows (both whole swizzle atoms)
@@ -161,12 +251,14 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map64
 }
 
 // Accumulator (TMEM lanes = output columns n0 .., columns = rows m0 ..) -> bf16 rows of y, by warps 0..3
-template <class Sm>
-__device__ __forceinline__ void store_unit(const Unit& t, uint32_t taddr, uint16_t* out_stage, Sm* sm,
-                                           uint64_t* acc_empty, __nv_bfloat16* __restrict__ y, int ldy) {
+// (columns from n0, rows m0 .. m1 - 1 of a tile `width` wide).  `release` is called by each warp once it has read its
+// part of the accumulator.
+template <class Release>
+__device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, uint32_t taddr, uint16_t* out_stage,
+                                           __nv_bfloat16* __restrict__ y, int ldy, Release release) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* st = out_stage + warp * (32 * 32);  // this warp's [32 rows][32 columns]
-  const int chunks = (t.width + 31) / 32;
+  const int chunks = (width + 31) / 32;
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
     uint32_t v[32];
@@ -174,7 +266,7 @@ __device__ __forceinline__ void store_unit(const Unit& t, uint32_t taddr, uint16
     if (c == chunks - 1) {  // read in full: the accumulator may be overwritten
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
+      if (lane == 0) release();
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) st[j * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
@@ -183,9 +275,9 @@ __device__ __forceinline__ void store_unit(const Unit& t, uint32_t taddr, uint16
     for (int i = 0; i < 4; ++i) {
       const int piece = lane + 32 * i;  // 128 pieces of 8 bf16
       const int r = piece >> 2, q = piece & 3;
-      const int m = t.m0 + c * 32 + r;
+      const int m = m0 + c * 32 + r;
       const uint4 o = *reinterpret_cast<const uint4*>(st + r * 32 + q * 8);
-      if (m < t.m1) *reinterpret_cast<uint4*>(y + (int64_t)m * ldy + t.n0 + warp * 32 + q * 8) = o;
+      if (m < m1) *reinterpret_cast<uint4*>(y + (int64_t)m * ldy + n0 + warp * 32 + q * 8) = o;
     }
     __syncwarp();
   }

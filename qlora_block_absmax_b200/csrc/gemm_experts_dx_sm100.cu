@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int acc = ucount & 1;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount >> 1) & 1, sm, err)) break;
       tc_fence_after();
-      store_unit(t, tmem + ((uint32_t)(warp * 32) << 16) + acc * TM, out_stage, sm, &sm->acc_empty[acc], dx, cols);
+      store_unit(t.n0, t.m0, t.m1, t.width, tmem + ((uint32_t)(warp * 32) << 16) + acc * TM, out_stage, dx, cols,
+                 [&]() { mbar_arrive(&sm->acc_empty[acc]); });
     }
   }
 

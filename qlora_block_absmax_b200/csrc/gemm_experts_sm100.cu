@@ -38,15 +38,21 @@ constexpr int kMmaWarp = kTmaWarp + 1;
 constexpr int kTmaWWarp = kTmaWarp + 2;
 constexpr int kThreads = (kTmaWWarp + 1) * 32;
 
-// TM: widest activation tile, 128, or 64 for few rows per expert (smaller stages leave room for a deeper code ring)
-template <int TM>
+// kPair: two CTAs share a tile of 256 weight rows x up to 256 activation rows (cta_group::2).  Each decodes its own 128
+// weight rows and loads half of the activation rows, so an SM loads 20 KB instead of 36 KB per 64 columns of a 256-row
+// tile; alone, a CTA with tiles of 256 rows was bound by those loads (790 cycles per 64 columns, 620 with a quarter of
+// them).  Otherwise tiles of up to 64 rows, for few rows per expert: smaller stages leave room for deeper rings.
+template <bool kPair>
 struct Cfg {
-  static constexpr int kStages = TM == 128 ? 3 : 6;    // operand ring: activation tile + 64 TMEM columns of weights
+  static constexpr int kTileM = kPair ? 256 : 64;       // activation rows per tile
+  static constexpr int kRowsB = kPair ? 128 : 64;       // of them in one CTA's shared memory
+  static constexpr int kTileCols = kPair ? 2 * kTileN : kTileN;
+  static constexpr int kStages = kPair ? 3 : 6;         // operand ring: activation tile + 64 TMEM columns of weights
   static constexpr int kWStages = 6;                    // packed codes
-  static constexpr int kAccs = 2;                      // accumulators: an epilogue runs beside the next tile
-  static constexpr int kHalfB = TM * kHalfK * 2;
+  static constexpr int kAccs = kPair ? 1 : 2;           // two accumulators: an epilogue runs beside the next tile
+  static constexpr int kHalfB = kRowsB * kHalfK * 2;
   static constexpr int kBBytes = 2 * kHalfB;
-  static constexpr int kACol0 = kAccs * TM;  // first TMEM column of the decoded tiles
+  static constexpr int kACol0 = kAccs * kTileM;  // first TMEM column of the decoded tiles
   static constexpr int kTmemCols = 512;
   static_assert(kACol0 + kStages * kTileK / 2 <= kTmemCols, "TMEM columns");
   // A parity wait tells two successive phases of a barrier apart, no more.  A group comes back to a ring kLanes
@@ -55,12 +61,13 @@ struct Cfg {
   static_assert(kStages >= kLanes && kWStages % kLanes == 0, "rings and producer groups");
 };
 
-template <int TM>
+template <bool kPair>
 struct Smem {
-  uint64_t wfull[Cfg<TM>::kWStages];
-  uint64_t wempty[Cfg<TM>::kWStages];
-  uint64_t full[Cfg<TM>::kStages];
-  uint64_t empty[Cfg<TM>::kStages];
+  uint64_t wfull[Cfg<kPair>::kWStages];
+  uint64_t wempty[Cfg<kPair>::kWStages];
+  uint64_t full[Cfg<kPair>::kStages];       // activation tile landed, weight tile written
+  uint64_t peer_full[Cfg<kPair>::kStages];  // (CTA 0 of a pair) the same in CTA 1, told by its MMA warp
+  uint64_t empty[Cfg<kPair>::kStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
@@ -71,34 +78,38 @@ struct Smem {
 // Shared memory: the packed codes, the epilogue's staging and Smem before the pair table at 64 KB, the activation ring
 // after it.  The window of a CTA without static shared memory starts at 1 KB (the kernel checks that all of it fits).
 constexpr uint32_t kWindow = 1024;
-template <int TM>
+template <bool kPair>
 constexpr size_t smem_bytes() {
-  return 2 * (size_t)kPairTable - kWindow + Cfg<TM>::kStages * Cfg<TM>::kBBytes;
+  return 2 * (size_t)kPairTable - kWindow + Cfg<kPair>::kStages * Cfg<kPair>::kBBytes;
 }
-template <int TM>
+template <bool kPair>
 constexpr uint32_t front_bytes() {
-  return Cfg<TM>::kWStages * kWBytes + kEpiWarps * kStageOutBytes + (uint32_t)sizeof(Smem<TM>);
+  return Cfg<kPair>::kWStages * kWBytes + kEpiWarps * kStageOutBytes + (uint32_t)sizeof(Smem<kPair>);
 }
-static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
-static_assert(kWindow + front_bytes<128>() <= kPairTable && kWindow + front_bytes<64>() <= kPairTable, "front part");
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory per CTA");
+static_assert(kWindow + front_bytes<true>() <= kPairTable && kWindow + front_bytes<false>() <= kPairTable, "front part");
 
-template <bool kDQ, int kBook, int TM>
+template <bool kDQ, int kBook, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_experts_kernel(Scales s, const int* __restrict__ offsets, int experts, int rows, int cols, int m_total,
                         const __grid_constant__ CUtensorMap xmap64, const __grid_constant__ CUtensorMap xmap16,
                         const __grid_constant__ CUtensorMap wmap, __nv_bfloat16* __restrict__ y, unsigned* err) {
-  using C = Cfg<TM>;
+  using C = Cfg<kPair>;
   constexpr int kStages = C::kStages, kWStages = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t front = (raw + 1023u) & ~1023u, table = kPairTable;
+  const uint32_t cta = raw & 0xff000000u;  // in a cluster, a CTA's window lies at its rank's place
+  const uint32_t front = (raw + 1023u) & ~1023u, table = cta + kPairTable;
   uint8_t* w_gen0 = smem_raw + (front - raw);
   const uint32_t w_smem0 = front, b_smem0 = table + kPairTable;
   uint16_t* out_stage = reinterpret_cast<uint16_t*>(w_gen0 + kWStages * kWBytes);
-  auto* sm = reinterpret_cast<Smem<TM>*>(w_gen0 + kWStages * kWBytes + kEpiWarps * kStageOutBytes);
+  auto* sm = reinterpret_cast<Smem<kPair>*>(w_gen0 + kWStages * kWBytes + kEpiWarps * kStageOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (front != kWindow) {  // the window does not start at 1 KB: refuse, touch nothing
+  const int rank = kPair ? (int)cluster_rank() : 0;
+  // the units of this CTA (or pair): u0, u0 + du, ...
+  const int u0 = kPair ? blockIdx.x >> 1 : blockIdx.x, du = kPair ? gridDim.x >> 1 : gridDim.x;
+  if (front != cta + kWindow) {  // the window does not start at 1 KB: refuse, touch nothing
     if (threadIdx.x == 0) atomicOr(err, kErrTimeout);
     return;
   }
@@ -110,27 +121,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm->full[i], 1 + 8);
+      mbar_init(&sm->peer_full[i], 1);
       mbar_init(&sm->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->acc_full[i], 1);
-      mbar_init(&sm->acc_empty[i], kEpiWarps);
+      mbar_init(&sm->acc_empty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
     sm->abort = 0;
     fence_mbar_init();
   }
   if (kDQ && threadIdx.x < 256) sm->unit_lut[threadIdx.x] = dq_unit(threadIdx.x, s.dq_code);
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
-                 "r"(C::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == kMmaWarp) tmem_alloc<kPair>(&sm->tmem_base, C::kTmemCols);
   fill_pair_table<kBook>(smem_raw + (table - raw));
   pdl_wait();
-  build_schedule<TM>(&sm->sc, offsets, experts, m_total, rows / kTileN);
+  build_schedule<C::kTileM>(&sm->sc, offsets, experts, m_total, (rows + C::kTileCols - 1) / C::kTileCols);
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   const int units = sm->sc.first[experts], kps = (cols + kTileK - 1) / kTileK;
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // apart.  A warp's rows lie in 32 different cache lines, so each load instruction costs as many lookups: the scale
     // codes come 16 at a time where rows of codes are 16-byte aligned (`vec`), a second-level scale only when the row
     // enters another block of 256.
-    int u = blockIdx.x, ks = group >> 1;  // the stage whose scale is loaded next
+    int u = u0, ks = group >> 1;  // the stage whose scale is loaded next
     const uint8_t* q_row = nullptr;       // (double quant) codes; s_row: second-level scale of the row's first block,
     const float* s_row = nullptr;         // s_off: that block's place among the 256; (plain) the row's scales
     uint32_t s_off = 0, s_at = ~0u;       // s_at: the second-level scale held
@@ -159,11 +167,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
       while (ks >= kps && u < units) {
         ks -= kps;
-        u += gridDim.x;
+        u += du;
       }
       if (u < units) {
-        const Unit t = unit_at<TM>(&sm->sc, experts, u);
-        const int64_t b = ((int64_t)t.expert * rows + t.n0 + p) * rb;
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        int n = t.n0 + rank * kTileN + p;
+        if (kPair && n >= rows) n = rows - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
+        const int64_t b = ((int64_t)t.expert * rows + n) * rb;
         if (kDQ) {
           q_row = s.q + b;
           s_row = s.scale + b / kDqBlock;
@@ -271,17 +281,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit t = unit_at<TM>(&sm->sc, experts, u);
+      for (int u = u0; u < units && ok; u += du) {
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
         for (int ks = 0; ks < kps; ++ks, ++it) {
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
           if (!ok) break;
           const int halves = odd && ks == kps - 1 ? 1 : 2;
-          mbar_expect_tx(&sm->full[as], (uint32_t)(t.width * halves) * kHalfK * 2);
+          const int width = kPair ? t.width / 2 : t.width;  // this CTA's rows of the tile
+          mbar_expect_tx(&sm->full[as], (uint32_t)(width * halves) * kHalfK * 2);
           for (int h = 0; h < halves; ++h)
-            load_rows(b_smem0 + as * C::kBBytes + h * C::kHalfB, &xmap64, &xmap16, ks * kTileK + h * kHalfK, t.m0,
-                      t.width, &sm->full[as]);
+            load_rows(b_smem0 + as * C::kBBytes + h * C::kHalfB, &xmap64, &xmap16, ks * kTileK + h * kHalfK,
+                      t.m0 + rank * width, width, &sm->full[as]);
         }
       }
       for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)  // drain the copies still in flight
@@ -292,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit t = unit_at<TM>(&sm->sc, experts, u);
-        const int n = t.expert * rows + t.n0;
+      for (int u = u0; u < units && ok; u += du) {
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        const int n = t.expert * rows + t.n0 + rank * kTileN;
         for (int ks = 0; ks < kps; ++ks, ++it) {
           const int ws = it % kWStages;
           ok = wait_or_abort(&sm->wempty[ws], ((it / kWStages) & 1) ^ 1, sm, err);
@@ -312,29 +323,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t bdesc0 = smem_desc_sw128(b_smem0);
     uint32_t as = 0, ph = 0, ucount = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++ucount) {
-      const uint32_t idesc = instr_desc(kTileN, __shfl_sync(0xffffffffu, unit_at<TM>(&sm->sc, experts, u).width, 0));
+    for (int u = u0; u < units && ok; u += du, ++ucount) {
+      const uint32_t idesc =
+          instr_desc(C::kTileCols,
+                     __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u).width, 0));
       const uint32_t acc = ucount % C::kAccs;
-      ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d_tm = tm_u + acc * TM;
+      if (rank == 0) {
+        if constexpr (kPair)
+          ok = wait_or_abort_cluster(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
+        else
+          ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t d_tm = tm_u + acc * C::kTileM;
       for (int ks = 0; ks < kps; ++ks) {
         ok = wait_or_abort(&sm->full[as], ph, sm, err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a_tm = tm_u + C::kACol0 + as * (kTileK / 2);
-        const uint64_t bdesc = bdesc0 + as * (C::kBBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kHalfK / 16; ++kk)
-            tc_mma_ts(d_tm, a_tm + kk * 8, bdesc + kk * 2, idesc, (ks | kk) != 0);
-          if (!odd || ks < kps - 1) {
-#pragma unroll
-            for (int kk = 0; kk < kHalfK / 16; ++kk)
-              tc_mma_ts(d_tm, a_tm + kHalfK / 2 + kk * 8, bdesc + (C::kHalfB >> 4) + kk * 2, idesc, 1);
+        if (kPair && rank == 1) {  // tell CTA 0, whose thread issues for both
+          tc_fence_before();
+          if (elect_one()) mbar_arrive_leader(&sm->peer_full[as]);
+        } else {
+          if constexpr (kPair) {
+            ok = wait_or_abort_cluster(&sm->peer_full[as], ph, sm, err);
+            if (!ok) break;
+            tc_fence_after();
           }
-          tc_commit(&sm->empty[as]);
+          const uint32_t a_tm = tm_u + C::kACol0 + as * (kTileK / 2);
+          const uint64_t bdesc = bdesc0 + as * (C::kBBytes >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kTileK / 16; ++kk) {
+              const int h = kk / (kHalfK / 16), j = kk % (kHalfK / 16);
+              if (h == 1 && odd && ks == kps - 1) break;
+              const uint64_t bd = bdesc + h * (C::kHalfB >> 4) + j * 2;
+              if constexpr (kPair)
+                tc_mma_ts_pair(d_tm, a_tm + kk * 8, bd, idesc, (ks | kk) != 0);
+              else
+                tc_mma_ts(d_tm, a_tm + kk * 8, bd, idesc, (ks | kk) != 0);
+            }
+            if constexpr (kPair)
+              tc_commit_pair(&sm->empty[as]);
+            else
+              tc_commit(&sm->empty[as]);
+          }
         }
         __syncwarp();
         if (++as == kStages) {
@@ -342,58 +375,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       }
-      if (ok && elect_one()) tc_commit(&sm->acc_full[acc]);
+      if (ok && rank == 0 && elect_one()) {
+        if constexpr (kPair)
+          tc_commit_pair(&sm->acc_full[acc]);
+        else
+          tc_commit(&sm->acc_full[acc]);
+      }
       __syncwarp();
     }
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++ucount) {
-      const Unit t = unit_at<TM>(&sm->sc, experts, u);
+    for (int u = u0; u < units; u += du, ++ucount) {
+      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
       const uint32_t acc = ucount % C::kAccs;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount / C::kAccs) & 1, sm, err)) break;
       tc_fence_after();
-      store_unit(t, tmem + ((uint32_t)(warp * 32) << 16) + acc * TM, out_stage, sm, &sm->acc_empty[acc], y, rows);
+      const int n0 = t.n0 + rank * kTileN;
+      store_unit(n0, t.m0, n0 < rows ? t.m1 : t.m0, t.width, tmem + ((uint32_t)(warp * 32) << 16) + acc * C::kTileM,
+                 out_stage, y, rows, [&]() {
+                   if (kPair && rank == 1)
+                     mbar_arrive_leader(&sm->acc_empty[acc]);
+                   else
+                     mbar_arrive(&sm->acc_empty[acc]);
+                 });
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA reads the other's shared memory or TMEM any more
   if (warp == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+    tmem_dealloc<kPair>(tmem, C::kTmemCols);
   }
 }
 
-template <bool kDQ, int kBook, int TM>
+template <bool kDQ, int kBook, bool kPair>
 cudaError_t launch(const ExpertsCall& c, const CUtensorMap& x64, const CUtensorMap& x16, const CUtensorMap& wmap,
                    int grid, unsigned* err, cudaStream_t stream) {
-  constexpr size_t smem = smem_bytes<TM>();
+  constexpr size_t smem = smem_bytes<kPair>();
   static std::atomic<uint64_t> attr_done{0};  // shared-memory opt-in, once per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(attr_done.load() & (1ull << dev))) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_experts_kernel<kDQ, kBook, TM>,
+    const cudaError_t e = cudaFuncSetAttribute(gemm_experts_kernel<kDQ, kBook, kPair>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(1ull << dev);
   }
   const cudaError_t e =
-      launch_pdl(gemm_experts_kernel<kDQ, kBook, TM>, dim3(grid), dim3(kThreads), smem, stream, c.scales, c.offsets,
-                 c.experts, (int)c.rows, (int)c.cols, (int)c.m, x64, x16, wmap, static_cast<__nv_bfloat16*>(c.out), err);
+      launch_pdl_cluster(gemm_experts_kernel<kDQ, kBook, kPair>, dim3(grid), dim3(kThreads), kPair ? 2 : 1, smem, stream,
+                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, x64, x16, wmap, static_cast<__nv_bfloat16*>(c.out), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int TM>
+template <bool kPair>
 cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& x64, const CUtensorMap& x16, const CUtensorMap& wmap,
                         int grid, unsigned* err, cudaStream_t stream) {
   const bool dq = c.scales.absmax == nullptr;
   if (dq)
-    return c.scales.book ? launch<true, 1, TM>(c, x64, x16, wmap, grid, err, stream)
-                         : launch<true, 0, TM>(c, x64, x16, wmap, grid, err, stream);
-  return c.scales.book ? launch<false, 1, TM>(c, x64, x16, wmap, grid, err, stream)
-                       : launch<false, 0, TM>(c, x64, x16, wmap, grid, err, stream);
+    return c.scales.book ? launch<true, 1, kPair>(c, x64, x16, wmap, grid, err, stream)
+                         : launch<true, 0, kPair>(c, x64, x16, wmap, grid, err, stream);
+  return c.scales.book ? launch<false, 1, kPair>(c, x64, x16, wmap, grid, err, stream)
+                       : launch<false, 0, kPair>(c, x64, x16, wmap, grid, err, stream);
 }
 
 }  // namespace
@@ -405,14 +451,15 @@ cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_
       !make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.packed, c.cols / 2, c.rows * c.experts, kTileK / 2, kTileN,
                 CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorNotSupported;
-  // no more units than the row tiles that m rows can make, each with all column tiles
-  const bool wide = c.m > 64 * (int64_t)c.experts;
-  const int64_t tm = wide ? 128 : 64;
+  // Pairs for many rows per expert.  No more units than the row tiles that m rows can make, each with all column tiles.
+  const bool pair = c.m > 64 * (int64_t)c.experts;
+  const int64_t tm = pair ? Cfg<true>::kTileM : Cfg<false>::kTileM, tn = pair ? 2 * kTileN : kTileN;
   const int64_t tiles = (c.m < c.experts ? c.m : c.experts) + c.m / tm;
-  const int64_t units = tiles * (c.rows / kTileN);
-  const int grid = (int)(units < num_sms ? units : num_sms);
-  return wide ? launch_form<128>(c, x64, x16, wmap, grid, err, stream)
-              : launch_form<64>(c, x64, x16, wmap, grid, err, stream);
+  const int64_t units = tiles * ((c.rows + tn - 1) / tn);
+  const int64_t most = pair ? num_sms / 2 : num_sms;
+  const int grid = (int)(units < most ? units : most) * (pair ? 2 : 1);
+  return pair ? launch_form<true>(c, x64, x16, wmap, grid, err, stream)
+              : launch_form<false>(c, x64, x16, wmap, grid, err, stream);
 }
 
 }  // namespace nf4
