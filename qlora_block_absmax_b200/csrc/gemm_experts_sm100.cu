@@ -329,10 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u).width, 0));
       const uint32_t acc = ucount % C::kAccs;
       if (rank == 0) {
-        if constexpr (kPair)
-          ok = wait_or_abort_cluster(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
-        else
-          ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
+        ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
         if (!ok) break;
         tc_fence_after();
       }
@@ -346,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) mbar_arrive_leader(&sm->peer_full[as]);
         } else {
           if constexpr (kPair) {
-            ok = wait_or_abort_cluster(&sm->peer_full[as], ph, sm, err);
+            ok = wait_or_abort(&sm->peer_full[as], ph, sm, err);
             if (!ok) break;
             tc_fence_after();
           }
