@@ -92,7 +92,7 @@ static_assert(kWindow + front_bytes<true>() <= kPairTable && kWindow + front_byt
 template <bool kDQ, int kBook, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_experts_kernel(Scales s, const int* __restrict__ offsets, int experts, int rows, int cols, int m_total,
-                        const __grid_constant__ CUtensorMap xmap64, const __grid_constant__ CUtensorMap xmap16,
+                        const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xmap16,
                         const __grid_constant__ CUtensorMap wmap, __nv_bfloat16* __restrict__ y, unsigned* err) {
   using C = Cfg<kPair>;
   constexpr int kStages = C::kStages, kWStages = C::kWStages;
@@ -288,11 +288,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
           if (!ok) break;
           const int halves = odd && ks == kps - 1 ? 1 : 2;
-          const int width = kPair ? t.width / 2 : t.width;  // this CTA's rows of the tile
-          mbar_expect_tx(&sm->full[as], (uint32_t)(width * halves) * kHalfK * 2);
-          for (int h = 0; h < halves; ++h)
-            load_rows(b_smem0 + as * C::kBBytes + h * C::kHalfB, &xmap64, &xmap16, ks * kTileK + h * kHalfK,
-                      t.m0 + rank * width, width, &sm->full[as]);
+          const uint32_t dst = b_smem0 + as * C::kBBytes;
+          if constexpr (kPair) {
+            // this CTA's half of the tile's rows; always a box of 128 (what lies behind the tile is loaded, not used:
+            // a box per stage and half is quicker than several smaller ones)
+            mbar_expect_tx(&sm->full[as], (uint32_t)halves * C::kHalfB);
+            for (int h = 0; h < halves; ++h)
+              tma_load_2d(dst + h * C::kHalfB, &xmap, ks * kTileK + h * kHalfK, t.m0 + rank * (t.width / 2),
+                          &sm->full[as]);
+          } else {
+            mbar_expect_tx(&sm->full[as], (uint32_t)(t.width * halves) * kHalfK * 2);
+            for (int h = 0; h < halves; ++h)
+              load_rows(dst + h * C::kHalfB, &xmap, &xmap16, ks * kTileK + h * kHalfK, t.m0, t.width, &sm->full[as]);
+          }
         }
       }
       for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)  // drain the copies still in flight
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDQ, int kBook, bool kPair>
-cudaError_t launch(const ExpertsCall& c, const CUtensorMap& x64, const CUtensorMap& x16, const CUtensorMap& wmap,
+cudaError_t launch(const ExpertsCall& c, const CUtensorMap& xbig, const CUtensorMap& x16, const CUtensorMap& wmap,
                    int grid, unsigned* err, cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<kPair>();
   static std::atomic<uint64_t> attr_done{0};  // shared-memory opt-in, once per device
@@ -423,40 +431,41 @@ cudaError_t launch(const ExpertsCall& c, const CUtensorMap& x64, const CUtensorM
   }
   const cudaError_t e =
       launch_pdl_cluster(gemm_experts_kernel<kDQ, kBook, kPair>, dim3(grid), dim3(kThreads), kPair ? 2 : 1, smem, stream,
-                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, x64, x16, wmap, static_cast<__nv_bfloat16*>(c.out), err);
+                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, xbig, x16, wmap, static_cast<__nv_bfloat16*>(c.out), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool kPair>
-cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& x64, const CUtensorMap& x16, const CUtensorMap& wmap,
+cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& xbig, const CUtensorMap& x16, const CUtensorMap& wmap,
                         int grid, unsigned* err, cudaStream_t stream) {
   const bool dq = c.scales.absmax == nullptr;
   if (dq)
-    return c.scales.book ? launch<true, 1, kPair>(c, x64, x16, wmap, grid, err, stream)
-                         : launch<true, 0, kPair>(c, x64, x16, wmap, grid, err, stream);
-  return c.scales.book ? launch<false, 1, kPair>(c, x64, x16, wmap, grid, err, stream)
-                       : launch<false, 0, kPair>(c, x64, x16, wmap, grid, err, stream);
+    return c.scales.book ? launch<true, 1, kPair>(c, xbig, x16, wmap, grid, err, stream)
+                         : launch<true, 0, kPair>(c, xbig, x16, wmap, grid, err, stream);
+  return c.scales.book ? launch<false, 1, kPair>(c, xbig, x16, wmap, grid, err, stream)
+                       : launch<false, 0, kPair>(c, xbig, x16, wmap, grid, err, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
-  CUtensorMap x64, x16, wmap;
-  if (!make_map(&x64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const bool pair = c.m > 64 * (int64_t)c.experts;  // many rows per expert
+  CUtensorMap xbig, x16, wmap;
+  if (!make_map(&xbig, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK,
+                pair ? Cfg<true>::kRowsB : Cfg<false>::kRowsB, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&x16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.packed, c.cols / 2, c.rows * c.experts, kTileK / 2, kTileN,
                 CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorNotSupported;
-  // Pairs for many rows per expert.  No more units than the row tiles that m rows can make, each with all column tiles.
-  const bool pair = c.m > 64 * (int64_t)c.experts;
+  // no more units than the row tiles that m rows can make, each with all column tiles
   const int64_t tm = pair ? Cfg<true>::kTileM : Cfg<false>::kTileM, tn = pair ? 2 * kTileN : kTileN;
   const int64_t tiles = (c.m < c.experts ? c.m : c.experts) + c.m / tm;
   const int64_t units = tiles * ((c.rows + tn - 1) / tn);
   const int64_t most = pair ? num_sms / 2 : num_sms;
   const int grid = (int)(units < most ? units : most) * (pair ? 2 : 1);
-  return pair ? launch_form<true>(c, x64, x16, wmap, grid, err, stream)
-              : launch_form<false>(c, x64, x16, wmap, grid, err, stream);
+  return pair ? launch_form<true>(c, xbig, x16, wmap, grid, err, stream)
+              : launch_form<false>(c, xbig, x16, wmap, grid, err, stream);
 }
 
 }  // namespace nf4
