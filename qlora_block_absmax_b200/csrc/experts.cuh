@@ -225,35 +225,79 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map64
   for (; r < width; r += 16) tma_load_2d(dst + r * 128, map16, x, m0 + r, bar);
 }
 
-// Accumulator (TMEM lanes = output columns n0 .., columns = rows m0 ..) -> bf16 rows of y, by warps 0..3
-// (columns from n0, rows m0 .. m1 - 1 of a tile `width` wide).  `release` is called by each warp once it has read its
-// part of the accumulator.
+// 16 lanes x 32 consecutive fp32 columns in the layout of an mma accumulator: registers 4i, 4i + 1 are lane L / 4,
+// columns 8i + 2 (L % 4) + {0, 1} of thread L, registers 4i + 2, 4i + 3 lane L / 4 + 8
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// The registers pass through the wait, so that no use of them is scheduled before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
+
+// four 8x8 matrices of 16-bit elements, stored transposed: lane L gives the address of row L % 8 of matrix L / 8
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+constexpr int kOutPitch = 80;                 // bytes per row of 32 bf16: 16 to spare, against bank conflicts
+constexpr int kOutBytes = 32 * kOutPitch;     // an epilogue warp's staging
+
+// Accumulator (TMEM lanes = output columns n0 .., columns = rows m0 .. m1 - 1 of a tile `width` wide) -> bf16 rows of
+// y, by warps 0..3.  The shared-memory pipe is the producers' busiest and this waits in the same queue, so the turn from
+// columns to rows takes few instructions: per 32x32 block four transposing matrix stores, four 16-byte loads and four
+// 16-byte stores to y (with a 2-byte shared store per value a 256-row tile took 4000 cycles, with 2-byte stores to y
+// 5300).  `release` is called by each warp once it has read its part of the accumulator: the tile's successor waits for
+// that.
 template <class Release>
-__device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, uint32_t taddr, uint16_t* out_stage,
+__device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, uint32_t taddr, uint8_t* stage_all,
                                            __nv_bfloat16* __restrict__ y, int ldy, Release release) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint16_t* st = out_stage + warp * (32 * 32);  // this warp's [32 rows][32 columns]
+  uint8_t* stage = stage_all + warp * kOutBytes;
+  // matrix q = lane / 8 of a store: rows (activation rows) 8 (q / 2) .., columns 8 (q % 2) ..
+  const uint32_t st = smem_u32(stage) + (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch + ((lane >> 3) & 1) * 16);
+  const int r0 = lane >> 2, q0 = lane & 3;  // this lane's pieces of the block: rows r0, r0 + 8, .., 16 bytes q0
+  __nv_bfloat16* p = y + (int64_t)(m0 + r0) * ldy + n0 + warp * 32 + q0 * 8;
   const int chunks = (width + 31) / 32;
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    uint32_t v[32];
-    tmem_ld32(taddr + c * 32, v);
+    uint32_t a[16], b[16];  // columns n 0..15 and 16..31 of the warp
+    tmem_ld_16x256(taddr + c * 32, a);
+    tmem_ld_16x256(taddr + (16u << 16) + c * 32, b);
+    tmem_ld_wait(a);
+    tmem_ld_wait(b);
     if (c == chunks - 1) {  // read in full: the accumulator may be overwritten
       tc_fence_before();
       __syncwarp();
       if (lane == 0) release();
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) st[j * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+    for (int h = 0; h < 2; ++h) {  // 16 activation rows
+      uint32_t pa[4], pb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pa[i] = pack_bf16x2(__uint_as_float(a[8 * h + 2 * i]), __uint_as_float(a[8 * h + 2 * i + 1]));
+        pb[i] = pack_bf16x2(__uint_as_float(b[8 * h + 2 * i]), __uint_as_float(b[8 * h + 2 * i + 1]));
+      }
+      stmatrix_x4_trans(st + h * 16 * kOutPitch, pa[0], pa[1], pa[2], pa[3]);
+      stmatrix_x4_trans(st + h * 16 * kOutPitch + 32, pb[0], pb[1], pb[2], pb[3]);
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int piece = lane + 32 * i;  // 128 pieces of 8 bf16
-      const int r = piece >> 2, q = piece & 3;
-      const int m = m0 + c * 32 + r;
-      const uint4 o = *reinterpret_cast<const uint4*>(st + r * 32 + q * 8);
-      if (m < m1) *reinterpret_cast<uint4*>(y + (int64_t)m * ldy + n0 + warp * 32 + q * 8) = o;
+      const uint4 o = *reinterpret_cast<const uint4*>(stage + (r0 + 8 * i) * kOutPitch + q0 * 16);
+      if (m0 + c * 32 + r0 + 8 * i < m1) *reinterpret_cast<uint4*>(p + (int64_t)(8 * i) * ldy) = o;
     }
+    p += (int64_t)32 * ldy;
     __syncwarp();
   }
 }

@@ -64,7 +64,7 @@ struct Smem {
 
 template <int TM>
 constexpr size_t smem_bytes() {
-  return (size_t)Cfg<TM>::kRingBytes + kEpiWarps * kStageOutBytes + sizeof(Smem<TM>) + 1024;
+  return (size_t)Cfg<TM>::kRingBytes + kEpiWarps * kOutBytes + sizeof(Smem<TM>) + 1024;
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
 
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_smem0 = base, a_smem0 = b_smem0 + kStages * C::kBBytes, w_smem0 = a_smem0 + kStages * kABytes;
   uint8_t* a_gen0 = gbase + kStages * C::kBBytes;
   const uint8_t* w_gen0 = a_gen0 + kStages * kABytes;
-  uint16_t* out_stage = reinterpret_cast<uint16_t*>(gbase + C::kRingBytes);
-  auto* sm = reinterpret_cast<Smem<TM>*>(gbase + C::kRingBytes + kEpiWarps * kStageOutBytes);
+  uint8_t* out_stage = gbase + C::kRingBytes;
+  auto* sm = reinterpret_cast<Smem<TM>*>(out_stage + kEpiWarps * kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {

@@ -84,7 +84,7 @@ constexpr size_t smem_bytes() {
 }
 template <bool kPair>
 constexpr uint32_t front_bytes() {
-  return Cfg<kPair>::kWStages * kWBytes + kEpiWarps * kStageOutBytes + (uint32_t)sizeof(Smem<kPair>);
+  return Cfg<kPair>::kWStages * kWBytes + kEpiWarps * kOutBytes + (uint32_t)sizeof(Smem<kPair>);
 }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory per CTA");
 static_assert(kWindow + front_bytes<true>() <= kPairTable && kWindow + front_bytes<false>() <= kPairTable, "front part");
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t front = (raw + 1023u) & ~1023u, table = cta + kPairTable;
   uint8_t* w_gen0 = smem_raw + (front - raw);
   const uint32_t w_smem0 = front, b_smem0 = table + kPairTable;
-  uint16_t* out_stage = reinterpret_cast<uint16_t*>(w_gen0 + kWStages * kWBytes);
-  auto* sm = reinterpret_cast<Smem<kPair>*>(w_gen0 + kWStages * kWBytes + kEpiWarps * kStageOutBytes);
+  uint8_t* out_stage = w_gen0 + kWStages * kWBytes;
+  auto* sm = reinterpret_cast<Smem<kPair>*>(out_stage + kEpiWarps * kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair ? (int)cluster_rank() : 0;
   // the units of this CTA (or pair): u0, u0 + du, ...
