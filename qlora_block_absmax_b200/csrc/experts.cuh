@@ -72,12 +72,16 @@ constexpr uint32_t kPairTable = 65536;  // bytes and alignment (the second half 
 
 __constant__ float c_code_experts[2][16] = {NF4_CODE_INIT, FP4_CODE_INIT};  // by code book
 
-template <int kBook>
+// The gradient keeps its decoded tiles in shared memory and has no 64 KB to spare: there the rows are 128 bytes, the
+// table 32 KB, and the address takes a shift and a LOP3 instead of the permute.
+constexpr uint32_t kPairTableDense = 32768;
+
+template <int kBook, int kRow = 256>
 __device__ __forceinline__ void fill_pair_table(uint8_t* table) {
   for (int i = threadIdx.x; i < 256 * 8; i += blockDim.x) {  // two copies of an entry
     const int v = i >> 3;
     const float hi = c_code_experts[kBook][v >> 4], lo = c_code_experts[kBook][v & 15];
-    *reinterpret_cast<float4*>(table + v * 256 + (i & 7) * 16) = make_float4(hi, lo, hi, lo);
+    *reinterpret_cast<float4*>(table + v * kRow + (i & 7) * 16) = make_float4(hi, lo, hi, lo);
   }
 }
 
@@ -99,6 +103,13 @@ __device__ __forceinline__ void decode_word_pairs(uint32_t w, uint32_t lane_base
   out[1] = scaled_pair(prmt(w, lane_base, 0x7614u), aa);
   out[2] = scaled_pair(prmt(w, lane_base, 0x7624u), aa);
   out[3] = scaled_pair(prmt(w, lane_base, 0x7634u), aa);
+}
+
+__device__ __forceinline__ void decode_word_pairs_dense(uint32_t w, uint32_t lane_base, uint64_t aa, uint32_t* out) {
+  out[0] = scaled_pair(((w << 7) & 0x7f80u) | lane_base, aa);
+  out[1] = scaled_pair(((w >> 1) & 0x7f80u) | lane_base, aa);
+  out[2] = scaled_pair(((w >> 9) & 0x7f80u) | lane_base, aa);
+  out[3] = scaled_pair(((w >> 17) & 0x7f80u) | lane_base, aa);
 }
 
 __device__ __forceinline__ uint64_t both(float a) {
@@ -182,6 +193,16 @@ __device__ __forceinline__ void tc_mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem,
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// the same with A (128 rows in each CTA) in shared memory
+__device__ __forceinline__ void tc_mma_ss_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
       : "memory");
 }
 
