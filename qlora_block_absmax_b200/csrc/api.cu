@@ -520,6 +520,13 @@ nf4_status check_experts(const nf4_weight* w, int32_t experts, int64_t m, bool g
   return NF4_OK;
 }
 
+// of the current device; a B200's where there is none
+int multiprocessors() {
+  DeviceInfo d;
+  const nf4_status st = device_info(&d);
+  return (st == NF4_OK || st == NF4_ERR_ARCH) && d.num_sms > 0 ? d.num_sms : 148;
+}
+
 using ExpertsLauncher = cudaError_t (*)(const nf4::ExpertsCall&, unsigned*, cudaStream_t, int);
 
 nf4_status run_experts(const nf4_weight* w, int32_t experts, const void* in, const int32_t* offsets, int64_t m,
@@ -531,13 +538,19 @@ nf4_status run_experts(const nf4_weight* w, int32_t experts, const void* in, con
   if (st != NF4_OK || empty) return st;
   if (in == nullptr || offsets == nullptr || out == nullptr) return NF4_ERR_INVALID_ARG;
   if (!aligned(in, 16) || !aligned(out, 16) || !aligned(offsets, 4)) return NF4_ERR_MISALIGNED;
-  (void)workspace;
-  (void)workspace_bytes;
   c.in = in;
   c.offsets = offsets;
   c.out = out;
+  c.workspace = nullptr;
   DeviceInfo d;
   if ((st = device_info(&d)) != NF4_OK) return st;
+  const size_t need = nf4::experts_workspace_bytes(m, experts, gradient ? c.cols : c.rows, gradient ? c.rows : c.cols,
+                                                   d.num_sms);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return NF4_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return NF4_ERR_MISALIGNED;
+    c.workspace = workspace;
+  }
   return from_cuda(launch(c, d.error_word, reinterpret_cast<cudaStream_t>(stream), d.num_sms));
 }
 
@@ -562,9 +575,15 @@ bool float_dtype(int32_t t) { return t == NF4_F32 || t == NF4_BF16 || t == NF4_F
 
 extern "C" {
 
-size_t nf4_gemm_experts_workspace_bytes(const nf4_weight* /*w*/, int32_t /*experts*/, int64_t /*m*/) { return 0; }
+size_t nf4_gemm_experts_workspace_bytes(const nf4_weight* w, int32_t experts, int64_t m) {
+  if (w == nullptr || experts < 1 || w->rows <= 0 || w->cols <= 0 || m <= 0) return 0;
+  return nf4::experts_workspace_bytes(m, experts, w->rows / experts, w->cols, multiprocessors());
+}
 
-size_t nf4_gemm_experts_dx_workspace_bytes(const nf4_weight* /*w*/, int32_t /*experts*/, int64_t /*m*/) { return 0; }
+size_t nf4_gemm_experts_dx_workspace_bytes(const nf4_weight* w, int32_t experts, int64_t m) {
+  if (w == nullptr || experts < 1 || w->rows <= 0 || w->cols <= 0 || m <= 0) return 0;
+  return nf4::experts_workspace_bytes(m, experts, w->cols, w->rows / experts, multiprocessors());
+}
 
 nf4_status nf4_gemm_experts(const nf4_weight* w, int32_t experts, const void* x, const int32_t* offsets, int64_t m,
                             void* y, void* workspace, size_t workspace_bytes, nf4_stream_t stream) {

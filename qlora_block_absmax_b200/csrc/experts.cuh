@@ -24,6 +24,32 @@ struct Schedule {
   int end[kMaxExperts];        // one past its last row
 };
 
+// Split reductions: with fewer than half as many units as CTAs (one token through two experts, say), each unit's
+// reduction is cut into `splits` items of at least kMinSplitStages stages, one item per CTA.  An item's fp32 accumulator
+// goes to the workspace; each epilogue warp (32 columns) that finds itself the last of its unit adds all of them in
+// order and stores the rows.  Nobody waits for another CTA, so launches that share the GPU cannot block one another.
+constexpr int kMinSplitStages = 4;
+constexpr int kPartialFloats = (int)(kExpertsPartialBytes / sizeof(float));
+static_assert(kPartialFloats == 64 * kTileN, "an item's accumulator: up to 64 rows x 128 columns");
+
+struct Split {
+  float* part;      // [items][kPartialFloats]
+  unsigned* count;  // arrivals per unit and epilogue warp
+};
+
+inline Split split_at(void* workspace) {
+  auto* w = static_cast<uint8_t*>(workspace);
+  return w == nullptr ? Split{nullptr, nullptr}
+                      : Split{reinterpret_cast<float*>(w + kExpertsCountBytes), reinterpret_cast<unsigned*>(w)};
+}
+
+__device__ __forceinline__ int split_of(int units, int grid, int kps, bool have) {
+  if (!have || units <= 0) return 1;
+  int s = grid / units;
+  s = s < kps / kMinSplitStages ? s : kps / kMinSplitStages;
+  return s < 1 ? 1 : s > kExpertsMaxSplit ? kExpertsMaxSplit : s;
+}
+
 struct Unit {
   int expert, n0;     // expert; first output column (of N, or of K for the gradient)
   int m0, m1, width;  // activation rows [m0, m1) of a tile `width` wide
@@ -273,34 +299,26 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 constexpr int kOutPitch = 80;                 // bytes per row of 32 bf16: 16 to spare, against bank conflicts
 constexpr int kOutBytes = 32 * kOutPitch;     // an epilogue warp's staging
 
-// Accumulator (TMEM lanes = output columns n0 .., columns = rows m0 .. m1 - 1 of a tile `width` wide) -> bf16 rows of
-// y, by warps 0..3.  The shared-memory pipe is the producers' busiest and this waits in the same queue, so the turn from
-// columns to rows takes few instructions: per 32x32 block four transposing matrix stores, four 16-byte loads and four
-// 16-byte stores to y (with a 2-byte shared store per value a 256-row tile took 4000 cycles, with 2-byte stores to y
-// 5300).  `release` is called by each warp once it has read its part of the accumulator: the tile's successor waits for
-// that.
-template <class Release>
-__device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, uint32_t taddr, uint8_t* stage_all,
-                                           __nv_bfloat16* __restrict__ y, int ldy, Release release) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* stage = stage_all + warp * kOutBytes;
-  // matrix q = lane / 8 of a store: rows (activation rows) 8 (q / 2) .., columns 8 (q % 2) ..
-  const uint32_t st = smem_u32(stage) + (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch + ((lane >> 3) & 1) * 16);
-  const int r0 = lane >> 2, q0 = lane & 3;  // this lane's pieces of the block: rows r0, r0 + 8, .., 16 bytes q0
-  __nv_bfloat16* p = y + (int64_t)(m0 + r0) * ldy + n0 + warp * 32 + q0 * 8;
-  const int chunks = (width + 31) / 32;
-#pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
-    uint32_t a[16], b[16];  // columns n 0..15 and 16..31 of the warp
-    tmem_ld_16x256(taddr + c * 32, a);
-    tmem_ld_16x256(taddr + (16u << 16) + c * 32, b);
-    tmem_ld_wait(a);
-    tmem_ld_wait(b);
-    if (c == chunks - 1) {  // read in full: the accumulator may be overwritten
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) release();
-    }
+// The epilogue of warps 0..3: accumulator (TMEM lanes = output columns, columns = activation rows) -> bf16 rows.  The
+// shared-memory pipe is the producers' busiest and this waits in the same queue, so the turn from columns to rows takes
+// few instructions: per 32x32 block four transposing matrix stores, four 16-byte loads and four 16-byte stores to y (with
+// a 2-byte shared store per value a 256-row tile took 4000 cycles, with 2-byte stores to y 5300, like this 3600).
+struct RowWriter {
+  uint8_t* stage;
+  uint32_t st;
+  int r0, q0;
+  __device__ __forceinline__ explicit RowWriter(uint8_t* stage_all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    stage = stage_all + warp * kOutBytes;
+    // matrix q = lane / 8 of a store: rows (activation rows) 8 (q / 2) .., columns 8 (q % 2) ..
+    st = smem_u32(stage) + (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch + ((lane >> 3) & 1) * 16);
+    r0 = lane >> 2;  // this lane's pieces of the block: rows r0, r0 + 8, .., 16 bytes q0
+    q0 = lane & 3;
+  }
+  // a, b: output columns 0..15 and 16..31 of the warp (tmem_ld_16x256) x 32 rows; `p`: their place in y, of which
+  // the first `left` rows are written
+  __device__ __forceinline__ void block(const uint32_t (&a)[16], const uint32_t (&b)[16], __nv_bfloat16* p, int ldy,
+                                        int left) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 activation rows
       uint32_t pa[4], pb[4];
@@ -316,10 +334,95 @@ __device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, ui
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 o = *reinterpret_cast<const uint4*>(stage + (r0 + 8 * i) * kOutPitch + q0 * 16);
-      if (m0 + c * 32 + r0 + 8 * i < m1) *reinterpret_cast<uint4*>(p + (int64_t)(8 * i) * ldy) = o;
+      if (r0 + 8 * i < left) *reinterpret_cast<uint4*>(p + (int64_t)(r0 + 8 * i) * ldy + q0 * 8) = o;
     }
-    p += (int64_t)32 * ldy;
     __syncwarp();
+  }
+};
+
+// Tile of output columns n0 .., rows m0 .. m1 - 1, `width` wide.  `release` is called by each warp once it has read its
+// part of the accumulator: the tile's successor waits for that.
+template <class Release>
+__device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, uint32_t taddr, uint8_t* stage_all,
+                                           __nv_bfloat16* __restrict__ y, int ldy, Release release) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowWriter out(stage_all);
+  __nv_bfloat16* p = y + (int64_t)m0 * ldy + n0 + warp * 32;
+  const int chunks = (width + 31) / 32;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t a[16], b[16];
+    tmem_ld_16x256(taddr + c * 32, a);
+    tmem_ld_16x256(taddr + (16u << 16) + c * 32, b);
+    tmem_ld_wait(a);
+    tmem_ld_wait(b);
+    if (c == chunks - 1) {  // read in full: the accumulator may be overwritten
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) release();
+    }
+    out.block(a, b, p, ldy, m1 - m0 - c * 32);
+    p += (int64_t)32 * ldy;
+  }
+}
+
+// The same for item `w` (of `splits` per unit) of a split reduction.
+template <class Release>
+__device__ __forceinline__ void store_split(int w, int splits, const Split& sp, int n0, int m0, int m1, int width,
+                                            uint32_t taddr, uint8_t* stage_all, __nv_bfloat16* __restrict__ y, int ldy,
+                                            Release release) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int chunks = (width + 31) / 32, unit = w / splits;
+  // [chunk][a, b][4][128 threads] of 16 bytes
+  auto slot = [&](int item, int c, int h, int i) {
+    return reinterpret_cast<uint4*>(sp.part + (size_t)item * kPartialFloats) + ((c * 2 + h) * 4 + i) * 128 + tid;
+  };
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[16];
+      tmem_ld_16x256(taddr + ((uint32_t)(16 * h) << 16) + c * 32, a);
+      tmem_ld_wait(a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __stcg(slot(w, c, h, i), make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) release();
+  __threadfence();
+  __syncwarp();
+  unsigned before = 0;
+  if (lane == 0) before = atomicAdd(sp.count + unit * kEpiWarps + warp, 1u);
+  if (__shfl_sync(0xffffffffu, before, 0) != (unsigned)splits - 1) return;
+  if (lane == 0) sp.count[unit * kEpiWarps + warp] = 0;  // ready for the next call
+  __threadfence();
+  const RowWriter out(stage_all);
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t v[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sum[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+      for (int k = 0; k < splits; ++k) {  // in order: the result does not depend on who came last
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 o = __ldcg(slot(unit * splits + k, c, h, i));
+          sum[4 * i] += __uint_as_float(o.x);
+          sum[4 * i + 1] += __uint_as_float(o.y);
+          sum[4 * i + 2] += __uint_as_float(o.z);
+          sum[4 * i + 3] += __uint_as_float(o.w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[h][i] = __float_as_uint(sum[i]);
+    }
+    out.block(v[0], v[1], y + (int64_t)(m0 + c * 32) * ldy + n0 + warp * 32, ldy, m1 - m0 - c * 32);
   }
 }
 

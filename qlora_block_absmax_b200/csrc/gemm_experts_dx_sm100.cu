@@ -11,7 +11,8 @@
 //   A = Wc^T tile [128 k (UMMA M, MN-major)] x [64 n], B = dY tile [rows] x [64 n] (TMA), D in TMEM.
 // Two accumulators: one tile's epilogue runs beside the next tile's MMAs.  Warp roles, CTA pairs, decode and pipeline as
 // in the forward product; here the shared-memory pipe also carries the decoded tile (128 wavefronts per stage besides the
-// table's 256).
+// table's 256), so half of each block goes through the byte-permute decode instead: 8 experts of 14336x4096, 4096 rows
+// 497 -> 455 us, 16 rows 182 -> 167 us (in the forward product the same cost 5 to 15 %).
 #include <cuda.h>
 
 #include <atomic>
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gemm_experts_dx_kernel(Scales s, const int* __restrict__ offsets, int experts, int rows, int cols, int m_total,
                            const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap ymap16,
                            const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap smap,
-                           __nv_bfloat16* __restrict__ dx, unsigned* err) {
+                           __nv_bfloat16* __restrict__ dx, Split split, unsigned* err) {
   using C = Cfg<kPair>;
   constexpr int kStages = C::kStages, kWStages = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
@@ -145,7 +146,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int units = sm->sc.first[experts], kps = rows / kTileR;
+  const int kps = rows / kTileR;
+  // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
+  const int splits = kPair ? 1 : split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
+  const int units = sm->sc.first[experts] * splits;
+  auto first_stage = [&](int w) { return kPair ? 0 : (w % splits) * kps / splits; };
+  auto end_stage = [&](int w) { return kPair ? kps : (w % splits + 1) * kps / splits; };
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
     // ------------------------------------------------ producers
@@ -154,20 +160,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = p & (kTileR - 1), h = p >> 6;  // weight row within the stage, 64-column half of the output tile
     const float mu = kDQ ? __ldg(s.mean) : 0.0f;
     const uint32_t lane_base = pair_lane(table);
+    const DecodeMul dm = decode_mul();
     const int rb = cols / kBlock;
     // this thread's 128-byte row of the A tile
     uint8_t* const a_row = a_gen0 + (r >> 3) * kKGroup + h * kMnAtom + (r & 7) * 128;
     const uint32_t swz = (uint32_t)(r & 7) << 4;
-    int u = u0, ks = group;  // the stage read next
+    int u = u0, ks = (u0 < units ? first_stage(u0) : 0) + group;  // the stage read next
     int64_t block0 = 0;      // level-1 block of this thread in the unit's first stage
     int kb = 0;              // its column of blocks
+    int kend = u0 < units ? end_stage(u0) : 0;  // end of the stages of item u
     auto settle = [&]() {    // move (u, ks) to the unit that holds the stage
-      while (ks >= kps && u < units) {
-        ks -= kps;
+      while (u < units && ks >= kend) {
+        ks -= kend;
         u += du;
+        if (u < units) {
+          ks += first_stage(u);
+          kend = end_stage(u);
+        }
       }
       if (u < units) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
         kb = (t.n0 + rank * kTileN) / kBlock + h;
         if (kPair && kb >= rb) kb = rb - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
         block0 = ((int64_t)t.expert * rows + r) * rb + kb;
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (more) {
       const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
       ks += kGroups;
-      if (ks >= kps) settle();
+      if (ks >= kend) settle();
       more = u < units;
       load_scale();
       if (more) more = load_codes();
@@ -240,8 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         *reinterpret_cast<uint4*>(arow + ((c << 4) ^ swz)) = make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
+      {  // the second half by byte permutes: the ALU pipe has room, the shared-memory pipe has not
+        const Table T = make_table<kBook>(__uint_as_float((uint32_t)aa));
 #pragma unroll
-      for (int c = 0; c < 4; ++c) decode_word_pairs_dense(words[4 + c], lane_base, aa, q + 4 * c);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t d[4];
+          decode_word(words[4 + c], T, d, dm);
+          q[4 * c] = d[0];
+          q[4 * c + 1] = d[1];
+          q[4 * c + 2] = d[2];
+          q[4 * c + 3] = d[3];
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         *reinterpret_cast<uint4*>(arow + (((c + 4) << 4) ^ swz)) =
@@ -262,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
-        for (int ks = 0; ks < kps; ++ks, ++it) {
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
           if (!ok) break;
@@ -286,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
         const int n = t.expert * rows, k0 = t.n0 + rank * kTileN;
-        for (int ks = 0; ks < kps; ++ks, ++it) {
+        for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int ws = it % kWStages;
           ok = wait_or_abort(&sm->wempty[ws], ((it / kWStages) & 1) ^ 1, sm, err);
           if (!ok) break;
@@ -311,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int u = u0; u < units && ok; u += du, ++ucount) {
       const uint32_t idesc = instr_desc(
-          C::kTileCols, __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u).width, 0),
+          C::kTileCols, __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits).width, 0),
           /*a_mn=*/true);
       const uint32_t acc = ucount & 1;
       if (rank == 0) {
@@ -320,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t d_tm = tm_u + acc * C::kTileM;
-      for (int ks = 0; ks < kps; ++ks) {
+      const int k0 = first_stage(u), k1 = end_stage(u);
+      for (int ks = k0; ks < k1; ++ks) {
         ok = wait_or_abort(&sm->full[as], ph, sm, err);
         if (!ok) break;
         tc_fence_after();
@@ -339,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < kTileR / 16; ++kk) {  // 16 weight rows per MMA: two 8-row groups, 32 bytes of dY
               const uint64_t ad = adesc + kk * (2 * kKGroup >> 4), bd = bdesc + kk * 2;
               if constexpr (kPair)
-                tc_mma_ss_pair(d_tm, ad, bd, idesc, (ks | kk) != 0);
+                tc_mma_ss_pair(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
               else
-                tc_mma_ss(d_tm, ad, bd, idesc, (ks | kk) != 0);
+                tc_mma_ss(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
             }
             if constexpr (kPair)
               tc_commit_pair(&sm->empty[as]);
@@ -367,18 +390,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
     for (int u = u0; u < units; u += du, ++ucount) {
-      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
       const uint32_t acc = ucount & 1;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount >> 1) & 1, sm, err)) break;
       tc_fence_after();
-      const int k0 = t.n0 + rank * kTileN;
-      store_unit(k0, t.m0, k0 < cols ? t.m1 : t.m0, t.width, tmem + ((uint32_t)(warp * 32) << 16) + acc * C::kTileM,
-                 out_stage, dx, cols, [&]() {
-                   if (kPair && rank == 1)
-                     mbar_arrive_leader(&sm->acc_empty[acc]);
-                   else
-                     mbar_arrive(&sm->acc_empty[acc]);
-                 });
+      const int n0 = t.n0 + rank * kTileN;  // first output column
+      const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16) + acc * C::kTileM;
+      auto release = [&]() {
+        if (kPair && rank == 1)
+          mbar_arrive_leader(&sm->acc_empty[acc]);
+        else
+          mbar_arrive(&sm->acc_empty[acc]);
+      };
+      if (kPair || splits == 1)
+        store_unit(n0, t.m0, n0 < cols ? t.m1 : t.m0, t.width, taddr, out_stage, dx, cols, release);
+      else
+        store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, dx, cols, release);
     }
   }
 
@@ -410,7 +437,7 @@ cudaError_t launch(const ExpertsCall& c, const Maps& m, int grid, unsigned* err,
   const cudaError_t e = launch_pdl_cluster(gemm_experts_dx_kernel<kDQ, kScaleTma, kBook, kPair>, dim3(grid),
                                            dim3(kThreads), kPair ? 2 : 1, smem, stream, c.scales, c.offsets, c.experts,
                                            (int)c.rows, (int)c.cols, (int)c.m, m.y, m.y16, m.w, m.s,
-                                           static_cast<__nv_bfloat16*>(c.out), err);
+                                           static_cast<__nv_bfloat16*>(c.out), split_at(c.workspace), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -430,7 +457,7 @@ cudaError_t launch_book(const ExpertsCall& c, const Maps& m, bool pair, int grid
 }  // namespace
 
 cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
-  const bool pair = c.m > 64 * (int64_t)c.experts;  // many rows per expert
+  const bool pair = experts_pair(c.m, c.experts);
   const bool dq = c.scales.absmax == nullptr;
   const int64_t rb = c.cols / kBlock, stack = c.rows * c.experts;
   Maps m;
@@ -451,7 +478,7 @@ cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStre
   // no more units than the row tiles that m rows can make, each with all column tiles
   const int64_t tm = pair ? Cfg<true>::kTileM : Cfg<false>::kTileM, tn = pair ? 2 * kTileN : kTileN;
   const int64_t tiles = (c.m < c.experts ? c.m : c.experts) + c.m / tm;
-  const int64_t units = tiles * ((c.cols + tn - 1) / tn);
+  const int64_t units = tiles * ((c.cols + tn - 1) / tn) * (c.workspace != nullptr ? kExpertsMaxSplit : 1);
   const int64_t most = pair ? num_sms / 2 : num_sms;
   const int grid = (int)(units < most ? units : most) * (pair ? 2 : 1);
   if (dq)

@@ -93,7 +93,7 @@ template <bool kDQ, int kBook, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_experts_kernel(Scales s, const int* __restrict__ offsets, int experts, int rows, int cols, int m_total,
                         const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xmap16,
-                        const __grid_constant__ CUtensorMap wmap, __nv_bfloat16* __restrict__ y, unsigned* err) {
+                        const __grid_constant__ CUtensorMap wmap, __nv_bfloat16* __restrict__ y, Split split, unsigned* err) {
   using C = Cfg<kPair>;
   constexpr int kStages = C::kStages, kWStages = C::kWStages;
   extern __shared__ uint8_t smem_raw[];
@@ -141,7 +141,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int units = sm->sc.first[experts], kps = (cols + kTileK - 1) / kTileK;
+  const int kps = (cols + kTileK - 1) / kTileK;
+  // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
+  const int splits = kPair ? 1 : split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
+  const int units = sm->sc.first[experts] * splits;
+  auto first_stage = [&](int w) { return kPair ? 0 : (w % splits) * kps / splits; };
+  auto end_stage = [&](int w) { return kPair ? kps : (w % splits + 1) * kps / splits; };
   const bool odd = cols % kTileK != 0;  // the last stage holds one block
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // apart.  A warp's rows lie in 32 different cache lines, so each load instruction costs as many lookups: the scale
     // codes come 16 at a time where rows of codes are 16-byte aligned (`vec`), a second-level scale only when the row
     // enters another block of 256.
-    int u = u0, ks = group >> 1;  // the stage whose scale is loaded next
+    int u = u0, ks = (u0 < units ? first_stage(u0) : 0) + (group >> 1);  // the stage whose scale is loaded next
     const uint8_t* q_row = nullptr;       // (double quant) codes; s_row: second-level scale of the row's first block,
     const float* s_row = nullptr;         // s_off: that block's place among the 256; (plain) the row's scales
     uint32_t s_off = 0, s_at = ~0u;       // s_at: the second-level scale held
@@ -164,13 +169,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 chunk = make_uint4(0, 0, 0, 0);
     uint32_t code = 0;
     float scale = 0.0f;
+    int kend = u0 < units ? end_stage(u0) : 0;  // end of the stages of item u
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
-      while (ks >= kps && u < units) {
-        ks -= kps;
+      while (u < units && ks >= kend) {
+        ks -= kend;
         u += du;
+        if (u < units) {
+          ks += first_stage(u);
+          kend = end_stage(u);
+        }
       }
       if (u < units) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
         int n = t.n0 + rank * kTileN + p;
         if (kPair && n >= rows) n = rows - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
         const int64_t b = ((int64_t)t.expert * rows + n) * rb;
@@ -250,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool some = 2 * ks + h < rb;
       const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
       ks += kLanes;
-      if (ks >= kps) settle();
+      if (ks >= kend) settle();
       more = u < units;
       load_scale();
       if (more) more = load_codes();
@@ -282,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
-        for (int ks = 0; ks < kps; ++ks, ++it) {
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
           if (!ok) break;
@@ -312,9 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
         const int n = t.expert * rows + t.n0 + rank * kTileN;
-        for (int ks = 0; ks < kps; ++ks, ++it) {
+        for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int ws = it % kWStages;
           ok = wait_or_abort(&sm->wempty[ws], ((it / kWStages) & 1) ^ 1, sm, err);
           if (!ok) break;
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u0; u < units && ok; u += du, ++ucount) {
       const uint32_t idesc =
           instr_desc(C::kTileCols,
-                     __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u).width, 0));
+                     __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits).width, 0));
       const uint32_t acc = ucount % C::kAccs;
       if (rank == 0) {
         ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
@@ -342,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t d_tm = tm_u + acc * C::kTileM;
-      for (int ks = 0; ks < kps; ++ks) {
+      const int k0 = first_stage(u), k1 = end_stage(u);
+      for (int ks = k0; ks < k1; ++ks) {
         ok = wait_or_abort(&sm->full[as], ph, sm, err);
         if (!ok) break;
         tc_fence_after();
@@ -364,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (h == 1 && odd && ks == kps - 1) break;
               const uint64_t bd = bdesc + h * (C::kHalfB >> 4) + j * 2;
               if constexpr (kPair)
-                tc_mma_ts_pair(d_tm, a_tm + kk * 8, bd, idesc, (ks | kk) != 0);
+                tc_mma_ts_pair(d_tm, a_tm + kk * 8, bd, idesc, ks > k0 || kk > 0);
               else
-                tc_mma_ts(d_tm, a_tm + kk * 8, bd, idesc, (ks | kk) != 0);
+                tc_mma_ts(d_tm, a_tm + kk * 8, bd, idesc, ks > k0 || kk > 0);
             }
             if constexpr (kPair)
               tc_commit_pair(&sm->empty[as]);
@@ -392,18 +403,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
     for (int u = u0; u < units; u += du, ++ucount) {
-      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u);
+      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
       const uint32_t acc = ucount % C::kAccs;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount / C::kAccs) & 1, sm, err)) break;
       tc_fence_after();
       const int n0 = t.n0 + rank * kTileN;
-      store_unit(n0, t.m0, n0 < rows ? t.m1 : t.m0, t.width, tmem + ((uint32_t)(warp * 32) << 16) + acc * C::kTileM,
-                 out_stage, y, rows, [&]() {
-                   if (kPair && rank == 1)
-                     mbar_arrive_leader(&sm->acc_empty[acc]);
-                   else
-                     mbar_arrive(&sm->acc_empty[acc]);
-                 });
+      const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16) + acc * C::kTileM;
+      auto release = [&]() {
+        if (kPair && rank == 1)
+          mbar_arrive_leader(&sm->acc_empty[acc]);
+        else
+          mbar_arrive(&sm->acc_empty[acc]);
+      };
+      if (kPair || splits == 1)
+        store_unit(n0, t.m0, n0 < rows ? t.m1 : t.m0, t.width, taddr, out_stage, y, rows, release);
+      else
+        store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, y, rows, release);
     }
   }
 
@@ -431,7 +446,7 @@ cudaError_t launch(const ExpertsCall& c, const CUtensorMap& xbig, const CUtensor
   }
   const cudaError_t e =
       launch_pdl_cluster(gemm_experts_kernel<kDQ, kBook, kPair>, dim3(grid), dim3(kThreads), kPair ? 2 : 1, smem, stream,
-                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, xbig, x16, wmap, static_cast<__nv_bfloat16*>(c.out), err);
+                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, xbig, x16, wmap, static_cast<__nv_bfloat16*>(c.out), split_at(c.workspace), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -450,7 +465,7 @@ cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& xbig, const CUt
 }  // namespace
 
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
-  const bool pair = c.m > 64 * (int64_t)c.experts;  // many rows per expert
+  const bool pair = experts_pair(c.m, c.experts);
   CUtensorMap xbig, x16, wmap;
   if (!make_map(&xbig, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK,
                 pair ? Cfg<true>::kRowsB : Cfg<false>::kRowsB, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -461,7 +476,7 @@ cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_
   // no more units than the row tiles that m rows can make, each with all column tiles
   const int64_t tm = pair ? Cfg<true>::kTileM : Cfg<false>::kTileM, tn = pair ? 2 * kTileN : kTileN;
   const int64_t tiles = (c.m < c.experts ? c.m : c.experts) + c.m / tm;
-  const int64_t units = tiles * ((c.rows + tn - 1) / tn);
+  const int64_t units = tiles * ((c.rows + tn - 1) / tn) * (c.workspace != nullptr ? kExpertsMaxSplit : 1);
   const int64_t most = pair ? num_sms / 2 : num_sms;
   const int grid = (int)(units < most ? units : most) * (pair ? 2 : 1);
   return pair ? launch_form<true>(c, xbig, x16, wmap, grid, err, stream)

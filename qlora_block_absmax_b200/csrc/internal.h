@@ -169,7 +169,19 @@ struct ExpertsCall {
   const void* in;      // [m, cols], or [m, rows] for the gradient
   int64_t m;           // >= 1
   void* out;           // [m, rows], or [m, cols]
+  void* workspace;     // experts_workspace_bytes, or null when that is 0
 };
+// CTA pairs with tiles of 256 rows for more than 64 rows per expert on average, else tiles of 64 rows
+inline bool experts_pair(int64_t m, int experts) { return m > 64 * (int64_t)experts; }
+// Split reductions (tiles of 64 rows only): arrival counters, then one fp32 accumulator per CTA.  They are open to
+// launches that can have fewer than half as many units as the GPU has SMs.
+constexpr int kExpertsMaxSplit = 8;
+constexpr size_t kExpertsCountBytes = 4096;
+constexpr size_t kExpertsPartialBytes = 64 * 128 * 4;
+inline size_t experts_workspace_bytes(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
+  if (experts_pair(m, experts) || out_cols / 128 * 2 > num_sms || reduction < 1024) return 0;
+  return kExpertsCountBytes + (size_t)num_sms * kExpertsPartialBytes;
+}
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
 cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
 

@@ -256,6 +256,31 @@ def test_two_streams_at_once():
     nf4.check_device_error()
 
 
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("counts", [[1, 0, 0, 0], [0, 1, 0, 1], [2, 2, 2, 2], [0, 64, 3, 0], [33, 0, 0, 40]])
+def test_few_units_split_the_reduction(gradient, counts):
+    """single tokens: fewer units than SMs, the reduction split over CTAs; one workspace for calls in a row, equal bits"""
+    n, k = (4096, 1024) if gradient else (1024, 4096 + 64)
+    qw, wc = make_stack(4, n, k)
+    off = offsets_of(counts)
+    f, size = ((nf4.gemm_experts_dx, nf4.gemm_experts_dx_workspace_bytes) if gradient else
+               (nf4.gemm_experts, nf4.gemm_experts_workspace_bytes))
+    x = activations(sum(counts), n if gradient else k, 17)
+    need = size(qw, 4, sum(counts))
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    y = f(qw, x, off, 4, workspace=ws)
+    check(y, *reference(wc, x, off, gradient), n if gradient else k)
+    for _ in range(10):
+        assert torch.equal(f(qw, x, off, 4, workspace=ws), y)
+    other = offsets_of(counts[::-1])
+    check(f(qw, x, other, 4, workspace=ws), *reference(wc, x, other, gradient), n if gradient else k)
+    assert torch.equal(f(qw, x, off, 4), y)  # a workspace of its own
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        f(qw, x, off, 4, workspace=ws[:need - 16])
+    nf4.check_device_error()
+
+
 def moe_forward(up, down, experts, x, off):
     """h = silu(gate) * value of the stacked [gate | value] rows, then the down projections; all rows sorted"""
     h = nf4.gemm_experts(up, x, off, experts).float()
