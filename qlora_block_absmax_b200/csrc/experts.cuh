@@ -24,30 +24,34 @@ struct Schedule {
   int end[kMaxExperts];        // one past its last row
 };
 
-// Split reductions: with fewer than half as many units as CTAs (one token through two experts, say), each unit's
-// reduction is cut into `splits` items of at least kMinSplitStages stages, one item per CTA.  An item's fp32 accumulator
-// goes to the workspace; each epilogue warp (32 columns) that finds itself the last of its unit adds all of them in
-// order and stores the rows.  Nobody waits for another CTA, so launches that share the GPU cannot block one another.
+// Split reductions: where the units do not fill the CTAs evenly (one token through two experts: 64 units of a 4096-row
+// weight on 148 SMs; 192 units would take two rounds), each unit's reduction is cut into `splits` items of at least
+// kMinSplitStages stages, and the items are dealt out instead.  An item's fp32 accumulator goes to the workspace; each
+// epilogue warp (32 columns) that finds itself the last of its unit adds all of them in order and stores the rows.
+// Nobody waits for another CTA, so launches that share the GPU cannot block one another.
 constexpr int kMinSplitStages = 4;
-constexpr int kPartialFloats = (int)(kExpertsPartialBytes / sizeof(float));
-static_assert(kPartialFloats == 64 * kTileN, "an item's accumulator: up to 64 rows x 128 columns");
-
 struct Split {
-  float* part;      // [items][kPartialFloats]
+  uint4* part;      // [items][pitch]: [chunk of 32 rows][column half][4][128 threads]
   unsigned* count;  // arrivals per unit and epilogue warp
+  int pitch;        // 16-byte pieces per item
 };
 
-inline Split split_at(void* workspace) {
-  auto* w = static_cast<uint8_t*>(workspace);
-  return w == nullptr ? Split{nullptr, nullptr}
-                      : Split{reinterpret_cast<float*>(w + kExpertsCountBytes), reinterpret_cast<unsigned*>(w)};
+inline Split split_at(const ExpertsCall& c) {
+  auto* w = static_cast<uint8_t*>(c.workspace);
+  if (w == nullptr) return Split{nullptr, nullptr, 0};
+  return Split{reinterpret_cast<uint4*>(w + kExpertsCountBytes), reinterpret_cast<unsigned*>(w),
+               (int)(experts_partial_bytes(c.m) / 16)};
 }
 
+// The number of splits whose rounds over the grid take the fewest stages; an item's exchange counts as three.  Lane s of
+// a warp looks at s + 1 splits.
 __device__ __forceinline__ int split_of(int units, int grid, int kps, bool have) {
-  if (!have || units <= 0) return 1;
-  int s = grid / units;
-  s = s < kps / kMinSplitStages ? s : kps / kMinSplitStages;
-  return s < 1 ? 1 : s > kExpertsMaxSplit ? kExpertsMaxSplit : s;
+  if (!have || units <= 0 || units > kExpertsItems * grid / 2) return 1;  // (two splits would be too many items)
+  const unsigned s = (threadIdx.x & (kExpertsMaxSplit - 1)) + 1, items = (unsigned)units * s;
+  unsigned cost = 0xffffffffu;
+  if (s == 1 || (items <= (unsigned)(kExpertsItems * grid) && kps >= (int)s * kMinSplitStages))
+    cost = ((items + grid - 1) / grid * ((kps + s - 1) / s + (s > 1 ? 3 : 0)) << 4) + (s - 1);
+  return (int)(__reduce_min_sync(0xffffffffu, cost) & 15u) + 1;
 }
 
 struct Unit {
@@ -373,9 +377,8 @@ __device__ __forceinline__ void store_split(int w, int splits, const Split& sp, 
                                             Release release) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int chunks = (width + 31) / 32, unit = w / splits;
-  // [chunk][a, b][4][128 threads] of 16 bytes
   auto slot = [&](int item, int c, int h, int i) {
-    return reinterpret_cast<uint4*>(sp.part + (size_t)item * kPartialFloats) + ((c * 2 + h) * 4 + i) * 128 + tid;
+    return sp.part + (size_t)item * sp.pitch + ((c * 2 + h) * 4 + i) * 128 + tid;
   };
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {

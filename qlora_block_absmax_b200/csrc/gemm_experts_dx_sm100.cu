@@ -65,6 +65,7 @@ struct Smem {
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
+  int splits;
   float unit_lut[256];
   Schedule sc;
 };
@@ -148,10 +149,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   const int kps = rows / kTileR;
   // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
-  const int splits = kPair ? 1 : split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
-  const int units = sm->sc.first[experts] * splits;
-  auto first_stage = [&](int w) { return kPair ? 0 : (w % splits) * kps / splits; };
-  auto end_stage = [&](int w) { return kPair ? kps : (w % splits + 1) * kps / splits; };
+  if (!kPair && warp == 0) {
+    const int n = split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
+    if (lane == 0) sm->splits = n;
+  }
+  if (!kPair) __syncthreads();
+  // read from shared memory where it is used, once per item: the producers have no register to spare for it
+  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->splits; };
+  const int units = sm->sc.first[experts] * n_splits();
+  auto first_stage = [&](int w) {
+    const int n = n_splits();
+    return n == 1 ? 0 : (w % n) * kps / n;
+  };
+  auto end_stage = [&](int w) {
+    const int n = n_splits();
+    return n == 1 ? kps : (w % n + 1) * kps / n;
+  };
+  auto unit_of = [&](int w) {
+    const int n = n_splits();
+    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, n == 1 ? w : w / n);
+  };
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
     // ------------------------------------------------ producers
@@ -179,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (u < units) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         kb = (t.n0 + rank * kTileN) / kBlock + h;
         if (kPair && kb >= rb) kb = rb - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
         block0 = ((int64_t)t.expert * rows + r) * rb + kb;
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
@@ -308,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         const int n = t.expert * rows, k0 = t.n0 + rank * kTileN;
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int ws = it % kWStages;
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int u = u0; u < units && ok; u += du, ++ucount) {
       const uint32_t idesc = instr_desc(
-          C::kTileCols, __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits).width, 0),
+          C::kTileCols, __shfl_sync(0xffffffffu, unit_of(u).width, 0),
           /*a_mn=*/true);
       const uint32_t acc = ucount & 1;
       if (rank == 0) {
@@ -390,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
     for (int u = u0; u < units; u += du, ++ucount) {
-      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+      const Unit t = unit_of(u);
       const uint32_t acc = ucount & 1;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount >> 1) & 1, sm, err)) break;
       tc_fence_after();
@@ -402,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&sm->acc_empty[acc]);
       };
-      if (kPair || splits == 1)
+      const int splits = n_splits();
+      if (splits == 1)
         store_unit(n0, t.m0, n0 < cols ? t.m1 : t.m0, t.width, taddr, out_stage, dx, cols, release);
       else
         store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, dx, cols, release);
@@ -437,7 +455,7 @@ cudaError_t launch(const ExpertsCall& c, const Maps& m, int grid, unsigned* err,
   const cudaError_t e = launch_pdl_cluster(gemm_experts_dx_kernel<kDQ, kScaleTma, kBook, kPair>, dim3(grid),
                                            dim3(kThreads), kPair ? 2 : 1, smem, stream, c.scales, c.offsets, c.experts,
                                            (int)c.rows, (int)c.cols, (int)c.m, m.y, m.y16, m.w, m.s,
-                                           static_cast<__nv_bfloat16*>(c.out), split_at(c.workspace), err);
+                                           static_cast<__nv_bfloat16*>(c.out), split_at(c), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

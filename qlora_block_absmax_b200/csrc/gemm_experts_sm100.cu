@@ -71,6 +71,7 @@ struct Smem {
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
+  int splits;
   float unit_lut[256];
   Schedule sc;
 };
@@ -143,10 +144,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   const int kps = (cols + kTileK - 1) / kTileK;
   // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
-  const int splits = kPair ? 1 : split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
-  const int units = sm->sc.first[experts] * splits;
-  auto first_stage = [&](int w) { return kPair ? 0 : (w % splits) * kps / splits; };
-  auto end_stage = [&](int w) { return kPair ? kps : (w % splits + 1) * kps / splits; };
+  if (!kPair && warp == 0) {
+    const int n = split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
+    if (lane == 0) sm->splits = n;
+  }
+  if (!kPair) __syncthreads();
+  // read from shared memory where it is used, once per item: the producers have no register to spare for it
+  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->splits; };
+  const int units = sm->sc.first[experts] * n_splits();
+  auto first_stage = [&](int w) {
+    const int n = n_splits();
+    return n == 1 ? 0 : (w % n) * kps / n;
+  };
+  auto end_stage = [&](int w) {
+    const int n = n_splits();
+    return n == 1 ? kps : (w % n + 1) * kps / n;
+  };
+  auto unit_of = [&](int w) {
+    const int n = n_splits();
+    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, n == 1 ? w : w / n);
+  };
   const bool odd = cols % kTileK != 0;  // the last stage holds one block
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (u < units) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         int n = t.n0 + rank * kTileN + p;
         if (kPair && n >= rows) n = rows - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
         const int64_t b = ((int64_t)t.expert * rows + n) * rb;
@@ -292,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
           ok = wait_or_abort(&sm->empty[as], ((it / kStages) & 1) ^ 1, sm, err);
@@ -322,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += du) {
-        const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+        const Unit t = unit_of(u);
         const int n = t.expert * rows + t.n0 + rank * kTileN;
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int ws = it % kWStages;
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u0; u < units && ok; u += du, ++ucount) {
       const uint32_t idesc =
           instr_desc(C::kTileCols,
-                     __shfl_sync(0xffffffffu, unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits).width, 0));
+                     __shfl_sync(0xffffffffu, unit_of(u).width, 0));
       const uint32_t acc = ucount % C::kAccs;
       if (rank == 0) {
         ok = wait_or_abort(&sm->acc_empty[acc], ((ucount / C::kAccs) & 1) ^ 1, sm, err);
@@ -403,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
     for (int u = u0; u < units; u += du, ++ucount) {
-      const Unit t = unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, u / splits);
+      const Unit t = unit_of(u);
       const uint32_t acc = ucount % C::kAccs;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount / C::kAccs) & 1, sm, err)) break;
       tc_fence_after();
@@ -415,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&sm->acc_empty[acc]);
       };
-      if (kPair || splits == 1)
+      const int splits = n_splits();
+      if (splits == 1)
         store_unit(n0, t.m0, n0 < rows ? t.m1 : t.m0, t.width, taddr, out_stage, y, rows, release);
       else
         store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, y, rows, release);
@@ -446,7 +464,7 @@ cudaError_t launch(const ExpertsCall& c, const CUtensorMap& xbig, const CUtensor
   }
   const cudaError_t e =
       launch_pdl_cluster(gemm_experts_kernel<kDQ, kBook, kPair>, dim3(grid), dim3(kThreads), kPair ? 2 : 1, smem, stream,
-                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, xbig, x16, wmap, static_cast<__nv_bfloat16*>(c.out), split_at(c.workspace), err);
+                         c.scales, c.offsets, c.experts, (int)c.rows, (int)c.cols, (int)c.m, xbig, x16, wmap, static_cast<__nv_bfloat16*>(c.out), split_at(c), err);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

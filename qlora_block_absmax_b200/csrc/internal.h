@@ -173,14 +173,17 @@ struct ExpertsCall {
 };
 // CTA pairs with tiles of 256 rows for more than 64 rows per expert on average, else tiles of 64 rows
 inline bool experts_pair(int64_t m, int experts) { return m > 64 * (int64_t)experts; }
-// Split reductions (tiles of 64 rows only): arrival counters, then one fp32 accumulator per CTA.  They are open to
-// launches that can have fewer than half as many units as the GPU has SMs.
+// Split reductions (tiles of 64 rows only): arrival counters, then one fp32 accumulator per item, at most kExpertsItems
+// per SM.
 constexpr int kExpertsMaxSplit = 8;
-constexpr size_t kExpertsCountBytes = 4096;
-constexpr size_t kExpertsPartialBytes = 64 * 128 * 4;
+constexpr int kExpertsItems = 4;
+constexpr size_t kExpertsCountBytes = 16384;  // items of two or more splits: at most 2 kExpertsItems units per SM
+inline size_t experts_partial_bytes(int64_t m) { return m > 32 ? 64 * 128 * 4 : 32 * 128 * 4; }
 inline size_t experts_workspace_bytes(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
-  if (experts_pair(m, experts) || out_cols / 128 * 2 > num_sms || reduction < 1024) return 0;
-  return kExpertsCountBytes + (size_t)num_sms * kExpertsPartialBytes;
+  // no split is worth its exchange where a unit is short, or where the fewest possible units make many rounds
+  if (experts_pair(m, experts) || reduction < 1024) return 0;
+  if ((m + 63) / 64 * (out_cols / 128) * 2 > (int64_t)kExpertsItems * num_sms) return 0;
+  return kExpertsCountBytes + (size_t)kExpertsItems * num_sms * experts_partial_bytes(m);
 }
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
 cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
