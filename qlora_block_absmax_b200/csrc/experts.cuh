@@ -22,6 +22,7 @@ struct Schedule {
   int first[kMaxExperts + 1];  // first unit of expert e; first[experts] = all units
   int row[kMaxExperts + 1];    // first row of expert e (offsets, held within the activations)
   int end[kMaxExperts];        // one past its last row
+  int splits;                  // items per unit
 };
 
 // Split reductions: where the units do not fill the CTAs evenly (one token through two experts: 64 units of a 4096-row
@@ -59,11 +60,12 @@ struct Unit {
   int m0, m1, width;  // activation rows [m0, m1) of a tile `width` wide
 };
 
-// All threads of the CTA; `ntn`: column tiles per expert.  Ends with a __syncthreads.  Offsets outside 0..m or
-// decreasing (a caller's error) are held to the range, so no tile reaches outside the activations.
+// All threads of the CTA; `ntn`: column tiles per expert, `kps`: stages per unit, `split`: split reductions are open.  The
+// caller synchronises the CTA afterwards.  Offsets outside 0..m or decreasing (a caller's error) are held to the range,
+// so no tile reaches outside the activations.
 template <int TM>
 __device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restrict__ offsets, int experts, int m,
-                                               int ntn) {
+                                               int ntn, int kps, bool split) {
   const int tid = threadIdx.x, lane = tid & 31;
   for (int e = tid; e < experts; e += blockDim.x) {
     int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
@@ -87,9 +89,16 @@ __device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restri
       if (e < experts) sc->first[e] = base + sum - own;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) sc->first[experts] = base;
+    const int splits = split_of(base, gridDim.x, kps, split);
+    if (lane == 0) {
+      sc->first[experts] = base;
+      sc->splits = splits;
+    }
   }
-  __syncthreads();
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // Decode through a shared table of fp32 code pairs: entry v (a byte of two codes) at 256 v, sixteen copies of 8 bytes,

@@ -71,7 +71,6 @@ struct Smem {
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort;
-  int splits;
   float unit_lut[256];
   Schedule sc;
 };
@@ -134,23 +133,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (kDQ && threadIdx.x < 256) sm->unit_lut[threadIdx.x] = dq_unit(threadIdx.x, s.dq_code);
   if (warp == kMmaWarp) tmem_alloc<kPair>(&sm->tmem_base, C::kTmemCols);
+  if (threadIdx.x == kTmaWarp * 32) {
+    prefetch_map(&xmap);
+    prefetch_map(&xmap16);
+    prefetch_map(&wmap);
+  }
   fill_pair_table<kBook>(smem_raw + (table - raw));
   pdl_wait();
-  build_schedule<C::kTileM>(&sm->sc, offsets, experts, m_total, (rows + C::kTileCols - 1) / C::kTileCols);
+  const int kps = (cols + kTileK - 1) / kTileK;
+  build_schedule<C::kTileM>(&sm->sc, offsets, experts, m_total, (rows + C::kTileCols - 1) / C::kTileCols, kps,
+                            !kPair && split.part != nullptr);
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int kps = (cols + kTileK - 1) / kTileK;
   // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
-  if (!kPair && warp == 0) {
-    const int n = split_of(sm->sc.first[experts], gridDim.x, kps, split.part != nullptr);
-    if (lane == 0) sm->splits = n;
-  }
-  if (!kPair) __syncthreads();
   // read from shared memory where it is used, once per item: the producers have no register to spare for it
-  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->splits; };
+  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->sc.splits; };
   const int units = sm->sc.first[experts] * n_splits();
   auto first_stage = [&](int w) {
     const int n = n_splits();
