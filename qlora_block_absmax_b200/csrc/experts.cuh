@@ -22,15 +22,20 @@ struct Schedule {
   int first[kMaxExperts + 1];  // first unit of expert e; first[experts] = all units
   int row[kMaxExperts + 1];    // first row of expert e (offsets, held within the activations)
   int end[kMaxExperts];        // one past its last row
-  int splits;                  // items per unit
+  int whole;                   // units that are one item each; the others are `splits` items each
+  int splits;
+  int items;
 };
 
-// Split reductions: where the units do not fill the CTAs evenly (one token through two experts: 64 units of a 4096-row
-// weight on 148 SMs; 192 units would take two rounds), each unit's reduction is cut into `splits` items of at least
-// kMinSplitStages stages, and the items are dealt out instead.  An item's fp32 accumulator goes to the workspace; each
-// epilogue warp (32 columns) that finds itself the last of its unit adds all of them in order and stores the rows.
-// Nobody waits for another CTA, so launches that share the GPU cannot block one another.
+// Split reductions (tiles of 64 rows).  The units are dealt out in rounds over the CTAs, and the last round is seldom full:
+// one token through two experts makes 64 units of a 4096-row weight for 148 SMs, 192 units make 1.3 rounds.  So the
+// reduction of each unit of the last round is cut into `splits` items of at least kMinSplitStages stages.  An item's fp32
+// accumulator goes to the workspace; each epilogue warp (32 columns) that finds itself the last of its unit adds all of
+// them in order and stores the rows.  Nobody waits for another CTA, so launches that share the GPU cannot block one
+// another.  (One row through each of two experts of 4096x14336: 58.9 -> 36 us; gradient of 16 rows, 8 experts of
+// 14336x4096: 161 -> 107 us.  Pairs gain nothing: a 256-row tile's exchange costs what the fuller round saves.)
 constexpr int kMinSplitStages = 4;
+
 struct Split {
   uint4* part;      // [items][pitch]: [chunk of 32 rows][column half][4][128 threads]
   unsigned* count;  // arrivals per unit and epilogue warp
@@ -44,11 +49,10 @@ inline Split split_at(const ExpertsCall& c) {
                (int)(experts_partial_bytes(c.m) / 16)};
 }
 
-// The number of splits whose rounds over the grid take the fewest stages; an item's exchange counts as three.  Lane s of
-// a warp looks at s + 1 splits.
-__device__ __forceinline__ int split_of(int units, int grid, int kps, bool have) {
-  if (!have || units <= 0 || units > kExpertsItems * grid / 2) return 1;  // (two splits would be too many items)
-  const unsigned s = (threadIdx.x & (kExpertsMaxSplit - 1)) + 1, items = (unsigned)units * s;
+// The number of splits of `rest` units whose rounds over the grid take the fewest stages; an item's exchange counts as
+// three of them.  Lane s of a warp looks at s + 1 splits.
+__device__ __forceinline__ int split_of(int rest, int grid, int kps) {
+  const unsigned s = (threadIdx.x & (kExpertsMaxSplit - 1)) + 1, items = (unsigned)rest * s;
   unsigned cost = 0xffffffffu;
   if (s == 1 || (items <= (unsigned)(kExpertsItems * grid) && kps >= (int)s * kMinSplitStages))
     cost = ((items + grid - 1) / grid * ((kps + s - 1) / s + (s > 1 ? 3 : 0)) << 4) + (s - 1);
@@ -89,10 +93,13 @@ __device__ __forceinline__ void build_schedule(Schedule* sc, const int* __restri
       if (e < experts) sc->first[e] = base + sum - own;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int splits = split_of(base, gridDim.x, kps, split);
+    const int rest = split ? base % (int)gridDim.x : 0;
+    const int splits = split_of(rest, gridDim.x, kps);
     if (lane == 0) {
       sc->first[experts] = base;
+      sc->whole = base - rest;
       sc->splits = splits;
+      sc->items = base - rest + rest * splits;
     }
   }
 }
@@ -328,21 +335,19 @@ struct RowWriter {
     r0 = lane >> 2;  // this lane's pieces of the block: rows r0, r0 + 8, .., 16 bytes q0
     q0 = lane & 3;
   }
-  // a, b: output columns 0..15 and 16..31 of the warp (tmem_ld_16x256) x 32 rows; `p`: their place in y, of which
-  // the first `left` rows are written
-  __device__ __forceinline__ void block(const uint32_t (&a)[16], const uint32_t (&b)[16], __nv_bfloat16* p, int ldy,
-                                        int left) const {
+  // 32 rows x output columns 16 half .. of the warp (as tmem_ld_16x256 gives them) into the staging
+  __device__ __forceinline__ void put(const uint32_t (&a)[16], int half) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 activation rows
-      uint32_t pa[4], pb[4];
+      uint32_t p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pa[i] = pack_bf16x2(__uint_as_float(a[8 * h + 2 * i]), __uint_as_float(a[8 * h + 2 * i + 1]));
-        pb[i] = pack_bf16x2(__uint_as_float(b[8 * h + 2 * i]), __uint_as_float(b[8 * h + 2 * i + 1]));
-      }
-      stmatrix_x4_trans(st + h * 16 * kOutPitch, pa[0], pa[1], pa[2], pa[3]);
-      stmatrix_x4_trans(st + h * 16 * kOutPitch + 32, pb[0], pb[1], pb[2], pb[3]);
+      for (int i = 0; i < 4; ++i)
+        p[i] = pack_bf16x2(__uint_as_float(a[8 * h + 2 * i]), __uint_as_float(a[8 * h + 2 * i + 1]));
+      stmatrix_x4_trans(st + h * 16 * kOutPitch + half * 32, p[0], p[1], p[2], p[3]);
     }
+  }
+  // the block to its place `p` in y, the first `left` rows of it
+  __device__ __forceinline__ void flush(__nv_bfloat16* p, int ldy, int left) const {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -374,18 +379,20 @@ __device__ __forceinline__ void store_unit(int n0, int m0, int m1, int width, ui
       __syncwarp();
       if (lane == 0) release();
     }
-    out.block(a, b, p, ldy, m1 - m0 - c * 32);
+    out.put(a, 0);
+    out.put(b, 1);
+    out.flush(p, ldy, m1 - m0 - c * 32);
     p += (int64_t)32 * ldy;
   }
 }
 
-// The same for item `w` (of `splits` per unit) of a split reduction.
+// The same for item r (of `splits` per unit) of the split units.
 template <class Release>
-__device__ __forceinline__ void store_split(int w, int splits, const Split& sp, int n0, int m0, int m1, int width,
+__device__ __forceinline__ void store_split(int r, int splits, const Split& sp, int n0, int m0, int m1, int width,
                                             uint32_t taddr, uint8_t* stage_all, __nv_bfloat16* __restrict__ y, int ldy,
                                             Release release) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int chunks = (width + 31) / 32, unit = w / splits;
+  const int chunks = (width + 31) / 32, unit = r / splits;
   auto slot = [&](int item, int c, int h, int i) {
     return sp.part + (size_t)item * sp.pitch + ((c * 2 + h) * 4 + i) * 128 + tid;
   };
@@ -398,7 +405,7 @@ __device__ __forceinline__ void store_split(int w, int splits, const Split& sp, 
       tmem_ld_wait(a);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        __stcg(slot(w, c, h, i), make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+        __stcg(slot(r, c, h, i), make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
     }
   }
   tc_fence_before();
@@ -407,15 +414,15 @@ __device__ __forceinline__ void store_split(int w, int splits, const Split& sp, 
   __threadfence();
   __syncwarp();
   unsigned before = 0;
-  if (lane == 0) before = atomicAdd(sp.count + unit * kEpiWarps + warp, 1u);
+  unsigned* const count = sp.count + unit * kEpiWarps + warp;
+  if (lane == 0) before = atomicAdd(count, 1u);
   if (__shfl_sync(0xffffffffu, before, 0) != (unsigned)splits - 1) return;
-  if (lane == 0) sp.count[unit * kEpiWarps + warp] = 0;  // ready for the next call
+  if (lane == 0) *count = 0;  // ready for the next call
   __threadfence();
   const RowWriter out(stage_all);
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    uint32_t v[2][16];
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       float sum[16];
 #pragma unroll
@@ -431,10 +438,12 @@ __device__ __forceinline__ void store_split(int w, int splits, const Split& sp, 
           sum[4 * i + 3] += __uint_as_float(o.w);
         }
       }
+      uint32_t v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[h][i] = __float_as_uint(sum[i]);
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[i]);
+      out.put(v, h);
     }
-    out.block(v[0], v[1], y + (int64_t)(m0 + c * 32) * ldy + n0 + warp * 32, ldy, m1 - m0 - c * 32);
+    out.flush(y + (int64_t)(m0 + c * 32) * ldy + n0 + warp * 32, ldy, m1 - m0 - c * 32);
   }
 }
 

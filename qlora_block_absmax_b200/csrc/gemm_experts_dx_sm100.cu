@@ -154,21 +154,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
-  // read from shared memory where it is used, once per item: the producers have no register to spare for it
-  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->sc.splits; };
-  const int units = sm->sc.first[experts] * n_splits();
+  // Items: the whole units, then `splits` per unit of the rest, split i taking stages [i * kps / splits, ...).  Read from
+  // shared memory where they are used, once per item: the producers have no registers to spare for them.
+  const volatile Schedule* const sv = &sm->sc;
+  const int items = sv->items;
   auto first_stage = [&](int w) {
-    const int n = n_splits();
-    return n == 1 ? 0 : (w % n) * kps / n;
+    if (kPair) return 0;
+    const int r = w - sv->whole, n = sv->splits;
+    return r < 0 || n == 1 ? 0 : r % n * kps / n;
   };
   auto end_stage = [&](int w) {
-    const int n = n_splits();
-    return n == 1 ? kps : (w % n + 1) * kps / n;
+    if (kPair) return kps;
+    const int r = w - sv->whole, n = sv->splits;
+    return r < 0 || n == 1 ? kps : (r % n + 1) * kps / n;
   };
   auto unit_of = [&](int w) {
-    const int n = n_splits();
-    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, n == 1 ? w : w / n);
+    if (!kPair) {
+      const int r = w - sv->whole, n = sv->splits;
+      if (r >= 0 && n > 1) w = sv->whole + r / n;
+    }
+    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, w);
   };
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
@@ -183,20 +188,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this thread's 128-byte row of the A tile
     uint8_t* const a_row = a_gen0 + (r >> 3) * kKGroup + h * kMnAtom + (r & 7) * 128;
     const uint32_t swz = (uint32_t)(r & 7) << 4;
-    int u = u0, ks = (u0 < units ? first_stage(u0) : 0) + group;  // the stage read next
+    int u = u0, ks = (u0 < items ? first_stage(u0) : 0) + group;  // the stage read next
     int64_t block0 = 0;      // level-1 block of this thread in the unit's first stage
     int kb = 0;              // its column of blocks
-    int kend = u0 < units ? end_stage(u0) : 0;  // end of the stages of item u
+    int kend = u0 < items ? end_stage(u0) : 0;  // end of the stages of item u
     auto settle = [&]() {    // move (u, ks) to the unit that holds the stage
-      while (u < units && ks >= kend) {
+      while (u < items && ks >= kend) {
         ks -= kend;
         u += du;
-        if (u < units) {
+        if (u < items) {
           ks += first_stage(u);
           kend = end_stage(u);
         }
       }
-      if (u < units) {
+      if (u < items) {
         const Unit t = unit_of(u);
         kb = (t.n0 + rank * kTileN) / kBlock + h;
         if (kPair && kb >= rb) kb = rb - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t code = 0;
     float scale = 0.0f;
     auto load_scale = [&]() {  // what of the block's scale lies in global memory
-      if (u >= units) return;
+      if (u >= items) return;
       const int64_t b = block0 + (int64_t)ks * kTileR * rb;
       if (kDQ) {
         if (!kScaleTma) code = __ldg(s.q + b);
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // software pipeline as in the forward product
     settle();
     load_scale();
-    bool more = u < units;
+    bool more = u < items;
     uint64_t aa = 0;
     if (more) {
       more = load_codes();
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
       ks += kGroups;
       if (ks >= kend) settle();
-      more = u < units;
+      more = u < items;
       load_scale();
       if (more) more = load_codes();
       uint8_t* const arow = a_row + as * kABytes;
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u0; u < units && ok; u += du) {
+      for (int u = u0; u < items && ok; u += du) {
         const Unit t = unit_of(u);
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u0; u < units && ok; u += du) {
+      for (int u = u0; u < items && ok; u += du) {
         const Unit t = unit_of(u);
         const int n = t.expert * rows, k0 = t.n0 + rank * kTileN;
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t adesc0 = smem_desc_mn_sw128(a_smem0, kMnAtom, kKGroup), bdesc0 = smem_desc_sw128(b_smem0);
     uint32_t as = 0, ph = 0, ucount = 0;
     bool ok = true;
-    for (int u = u0; u < units && ok; u += du, ++ucount) {
+    for (int u = u0; u < items && ok; u += du, ++ucount) {
       const uint32_t idesc = instr_desc(
           C::kTileCols, __shfl_sync(0xffffffffu, unit_of(u).width, 0),
           /*a_mn=*/true);
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
-    for (int u = u0; u < units; u += du, ++ucount) {
+    for (int u = u0; u < items; u += du, ++ucount) {
       const Unit t = unit_of(u);
       const uint32_t acc = ucount & 1;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount >> 1) & 1, sm, err)) break;
@@ -420,11 +425,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&sm->acc_empty[acc]);
       };
-      const int splits = n_splits();
-      if (splits == 1)
-        store_unit(n0, t.m0, n0 < cols ? t.m1 : t.m0, t.width, taddr, out_stage, dx, cols, release);
+      const int m1 = n0 < cols ? t.m1 : t.m0;  // (CTA 1 of an odd last column tile stores nothing)
+      const int r = kPair ? -1 : u - sv->whole, splits = kPair ? 1 : sv->splits;
+      if (kPair || r < 0 || splits == 1)
+        store_unit(n0, t.m0, m1, t.width, taddr, out_stage, dx, cols, release);
       else
-        store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, dx, cols, release);
+        store_split(r, splits, split, n0, t.m0, m1, t.width, taddr, out_stage, dx, cols, release);
     }
   }
 

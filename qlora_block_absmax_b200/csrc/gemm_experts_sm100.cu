@@ -148,23 +148,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // the other CTA's barriers are initialised, its TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  // items: unit * splits + split, the split's stages [split * kps / splits, ...); pairs never split
-  // read from shared memory where it is used, once per item: the producers have no register to spare for it
-  auto n_splits = [&]() { return kPair ? 1 : *(volatile int*)&sm->sc.splits; };
-  const int units = sm->sc.first[experts] * n_splits();
+  // Items: the whole units, then `splits` per unit of the rest, split i taking stages [i * kps / splits, ...).  Read from
+  // shared memory where they are used, once per item: the producers have no registers to spare for them.
+  const bool odd = cols % kTileK != 0;  // the last stage holds one block
+  const volatile Schedule* const sv = &sm->sc;
+  const int items = sv->items;
   auto first_stage = [&](int w) {
-    const int n = n_splits();
-    return n == 1 ? 0 : (w % n) * kps / n;
+    if (kPair) return 0;
+    const int r = w - sv->whole, n = sv->splits;
+    return r < 0 || n == 1 ? 0 : r % n * kps / n;
   };
   auto end_stage = [&](int w) {
-    const int n = n_splits();
-    return n == 1 ? kps : (w % n + 1) * kps / n;
+    if (kPair) return kps;
+    const int r = w - sv->whole, n = sv->splits;
+    return r < 0 || n == 1 ? kps : (r % n + 1) * kps / n;
   };
   auto unit_of = [&](int w) {
-    const int n = n_splits();
-    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, n == 1 ? w : w / n);
+    if (!kPair) {
+      const int r = w - sv->whole, n = sv->splits;
+      if (r >= 0 && n > 1) w = sv->whole + r / n;
+    }
+    return unit_at<C::kTileM, C::kTileCols>(&sm->sc, experts, w);
   };
-  const bool odd = cols % kTileK != 0;  // the last stage holds one block
 
   if (warp >= kProdWarp0 && warp < kTmaWarp) {
     // ------------------------------------------------ producers
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // apart.  A warp's rows lie in 32 different cache lines, so each load instruction costs as many lookups: the scale
     // codes come 16 at a time where rows of codes are 16-byte aligned (`vec`), a second-level scale only when the row
     // enters another block of 256.
-    int u = u0, ks = (u0 < units ? first_stage(u0) : 0) + (group >> 1);  // the stage whose scale is loaded next
+    int u = u0, ks = (u0 < items ? first_stage(u0) : 0) + (group >> 1);  // the stage whose scale is loaded next
     const uint8_t* q_row = nullptr;       // (double quant) codes; s_row: second-level scale of the row's first block,
     const float* s_row = nullptr;         // s_off: that block's place among the 256; (plain) the row's scales
     uint32_t s_off = 0, s_at = ~0u;       // s_at: the second-level scale held
@@ -186,17 +191,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 chunk = make_uint4(0, 0, 0, 0);
     uint32_t code = 0;
     float scale = 0.0f;
-    int kend = u0 < units ? end_stage(u0) : 0;  // end of the stages of item u
+    int kend = u0 < items ? end_stage(u0) : 0;  // end of the stages of item u
     auto settle = [&]() {  // move (u, ks) to the unit that holds the stage
-      while (u < units && ks >= kend) {
+      while (u < items && ks >= kend) {
         ks -= kend;
         u += du;
-        if (u < units) {
+        if (u < items) {
           ks += first_stage(u);
           kend = end_stage(u);
         }
       }
-      if (u < units) {
+      if (u < items) {
         const Unit t = unit_of(u);
         int n = t.n0 + rank * kTileN + p;
         if (kPair && n >= rows) n = rows - 1;  // an odd last column tile: CTA 1 decodes anything, and stores nothing
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto load_scale = [&]() {  // of block 2 ks + h; the second block of an odd reduction's last stage does not exist
       const int b = 2 * ks + h;
-      if (u >= units || b >= rb) return;
+      if (u >= items || b >= rb) return;
       if (kDQ) {
         if (vec) {
           if (b % 16 < 2 * kLanes) chunk = __ldg(reinterpret_cast<const uint4*>(q_row + (b & ~15)));
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the two halves' lookups wait for their own round.
     settle();
     load_scale();
-    bool more = u < units;
+    bool more = u < items;
     uint64_t aa = 0;
     if (more) {
       aa = block_scale(block_unit());
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t words[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
       ks += kLanes;
       if (ks >= kend) settle();
-      more = u < units;
+      more = u < items;
       load_scale();
       if (more) more = load_codes();
       const uint32_t ta = ta0 + as * (kTileK / 2);  // column j: codes 2j, 2j + 1 of the block as bf16x2
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u0; u < units && ok; u += du) {
+      for (int u = u0; u < items && ok; u += du) {
         const Unit t = unit_of(u);
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
           const int as = it % kStages;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u0; u < units && ok; u += du) {
+      for (int u = u0; u < items && ok; u += du) {
         const Unit t = unit_of(u);
         const int n = t.expert * rows + t.n0 + rank * kTileN;
         for (int ks = first_stage(u), e = end_stage(u); ks < e; ++ks, ++it) {
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t bdesc0 = smem_desc_sw128(b_smem0);
     uint32_t as = 0, ph = 0, ucount = 0;
     bool ok = true;
-    for (int u = u0; u < units && ok; u += du, ++ucount) {
+    for (int u = u0; u < items && ok; u += du, ++ucount) {
       const uint32_t idesc =
           instr_desc(C::kTileCols,
                      __shfl_sync(0xffffffffu, unit_of(u).width, 0));
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------ epilogue
     uint32_t ucount = 0;
-    for (int u = u0; u < units; u += du, ++ucount) {
+    for (int u = u0; u < items; u += du, ++ucount) {
       const Unit t = unit_of(u);
       const uint32_t acc = ucount % C::kAccs;
       if (!wait_or_abort(&sm->acc_full[acc], (ucount / C::kAccs) & 1, sm, err)) break;
@@ -432,11 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&sm->acc_empty[acc]);
       };
-      const int splits = n_splits();
-      if (splits == 1)
-        store_unit(n0, t.m0, n0 < rows ? t.m1 : t.m0, t.width, taddr, out_stage, y, rows, release);
+      const int m1 = n0 < rows ? t.m1 : t.m0;  // (CTA 1 of an odd last column tile stores nothing)
+      const int r = kPair ? -1 : u - sv->whole, splits = kPair ? 1 : sv->splits;
+      if (kPair || r < 0 || splits == 1)
+        store_unit(n0, t.m0, m1, t.width, taddr, out_stage, y, rows, release);
       else
-        store_split(u, splits, split, n0, t.m0, t.m1, t.width, taddr, out_stage, y, rows, release);
+        store_split(r, splits, split, n0, t.m0, m1, t.width, taddr, out_stage, y, rows, release);
     }
   }
 

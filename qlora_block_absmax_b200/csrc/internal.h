@@ -174,15 +174,15 @@ struct ExpertsCall {
 // CTA pairs with tiles of 256 rows for more than 64 rows per expert on average, else tiles of 64 rows
 inline bool experts_pair(int64_t m, int experts) { return m > 64 * (int64_t)experts; }
 // Split reductions (tiles of 64 rows only): arrival counters, then one fp32 accumulator per item, at most kExpertsItems
-// per SM.
+// items per SM.
 constexpr int kExpertsMaxSplit = 8;
 constexpr int kExpertsItems = 4;
-constexpr size_t kExpertsCountBytes = 16384;  // items of two or more splits: at most 2 kExpertsItems units per SM
+constexpr size_t kExpertsCountBytes = 4096;  // fewer split units than SMs, 4 counters each
 inline size_t experts_partial_bytes(int64_t m) { return m > 32 ? 64 * 128 * 4 : 32 * 128 * 4; }
 inline size_t experts_workspace_bytes(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
-  // no split is worth its exchange where a unit is short, or where the fewest possible units make many rounds
-  if (experts_pair(m, experts) || reduction < 1024) return 0;
-  if ((m + 63) / 64 * (out_cols / 128) * 2 > (int64_t)kExpertsItems * num_sms) return 0;
+  // no split is worth its exchange where a unit is short, and little where even the fewest possible units make many rounds
+  if (experts_pair(m, experts) || reduction < 1024 || num_sms > 255) return 0;
+  if ((m + 63) / 64 * (out_cols / 128) > 8 * (int64_t)num_sms) return 0;
   return kExpertsCountBytes + (size_t)kExpertsItems * num_sms * experts_partial_bytes(m);
 }
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
