@@ -60,14 +60,21 @@ def _need_cuda(t: torch.Tensor, name: str) -> None:
 _SAME_DEVICE = contextlib.nullcontext()
 
 
-def _on_device(t: torch.Tensor):
-    """The tensor's CUDA device as the current one (a no-op when it already is)."""
+def _on_device(t: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):
+    """The tensor's CUDA device as the current one and, where a stream is given, that stream too, so that what the call
+    allocates belongs to it (a no-op for the current device and stream)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
     return _SAME_DEVICE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.get_device())
 
 
 def _raw_stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
     """The handle of `stream`, or of the current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream.device_index != t.get_device():
+        raise ValueError("the stream must be on the tensors' device")
+    return stream.cuda_stream
 
 
 def _need_out(out: torch.Tensor, shape, like: torch.Tensor, dtype: Optional[torch.dtype] = None) -> None:
@@ -394,7 +401,7 @@ def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offset
     if x.dim() < 1 or x.shape[-1] != width:
         raise ValueError(f"the activations' last dimension must be {width}")
     m = x.numel() // width if width else 0
-    with _on_device(x):
+    with _on_device(x, stream):
         d = ctypes.byref(qw.descriptor())
         if out is None:
             out = x.new_empty((m, owidth))
@@ -503,7 +510,7 @@ def quantize_groups(w: torch.Tensor, group: int = 128, symmetric: bool = False,
     rows, cols = w.shape
     if group not in (32, 64, 128) or cols % group:
         raise ValueError("group must be 32, 64 or 128 and divide cols")
-    with _on_device(w):
+    with _on_device(w, stream):
         packed = w.new_empty((rows, cols // 2), dtype=torch.uint8)
         scale = w.new_empty((rows, cols // group), dtype=scale_dtype)
         zero = None if symmetric else w.new_empty((rows, cols // group), dtype=torch.uint8)
@@ -520,7 +527,7 @@ def dequantize_groups(gw: GroupWeight, dtype: torch.dtype = torch.float32, out=N
     if dtype not in _FLOAT_CODES:
         raise TypeError("dequantize_groups produces float32, bfloat16 or float16")
     d = gw.descriptor()
-    with _on_device(gw.packed):
+    with _on_device(gw.packed, stream):
         if out is None:
             out = gw.packed.new_empty((gw.rows, gw.cols), dtype=dtype)
         else:
@@ -544,7 +551,7 @@ def gemv_groups(gw: GroupWeight, x: torch.Tensor, out=None, stream=None) -> torc
         raise ValueError("x must have cols columns")
     d = gw.descriptor()
     batch = x.numel() // cols if cols else x.shape[:-1].numel()
-    with _on_device(x):
+    with _on_device(x, stream):
         if out is None:
             out = x.new_empty((batch, rows))
         else:

@@ -120,6 +120,41 @@ def test_short_and_long_reductions(n, k):
     nf4.check_device_error()
 
 
+@pytest.mark.parametrize("out_cols", [128, 384, 640])
+@pytest.mark.parametrize("red", [64, 192, 1024])
+@pytest.mark.parametrize("gradient", [False, True])
+def test_pairs_at_odd_widths(out_cols, red, gradient):
+    """many rows per expert (CTA pairs share 256 output columns): a last column tile of 128, one or three blocks of
+    reduction, tiles of 16 to 256 rows, the last expert's weight at the end of the stack"""
+    counts = [257, 1, 0, 130, 512, 31]
+    n, k = (red, out_cols) if gradient else (out_cols, red)
+    qw, wc = make_stack(len(counts), n, k, seed=5)
+    off = offsets_of(counts, lead=3)
+    x = activations(sum(counts) + 5, n if gradient else k, 18)
+    f = nf4.gemm_experts_dx if gradient else nf4.gemm_experts
+    out = torch.full((x.shape[0], out_cols), 3.5, dtype=torch.bfloat16, device="cuda")
+    f(qw, x, off, len(counts), out=out)
+    check(out, *reference(wc, x, off, gradient), red)
+    assert bool((out[:3] == 3.5).all()) and bool((out[-2:] == 3.5).all())
+    for _ in range(3):
+        assert torch.equal(f(qw, x, off, len(counts), out=out.clone()), out)
+    nf4.check_device_error()
+
+
+def test_side_stream_argument():
+    """stream=: the output is allocated and written on that stream"""
+    qw, wc = make_stack(2, 128, 128)
+    x, off = activations(60, 128, 19), offsets_of([20, 40])
+    ref = reference(wc, x, off, False)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = nf4.gemm_experts(qw, x, off, 2, stream=side)
+    dx = nf4.gemm_experts_dx(qw, x, off, 2, stream=side)
+    side.synchronize()
+    check(y, *ref, 128)
+    check(dx, *reference(wc, x, off, True), 128)
+
+
 @pytest.mark.parametrize("gradient", [False, True])
 def test_many_tiles_per_cta(gradient):
     """several hundred units on the grid: every CTA walks many tiles of several experts, repeated calls agree bit for bit"""

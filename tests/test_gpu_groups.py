@@ -199,6 +199,38 @@ def test_gemv_groups_unaligned_meta_and_stream_and_graph():
         assert torch.equal(out, nf4.gemv_groups(base, x))
 
 
+def test_quantize_groups_ties():
+    """16-bit weights on a grid of half steps of their scale: nearly every quotient is a tie, rounded to even as the
+    division would"""
+    g = np.random.default_rng(9)
+    for dtype in (torch.bfloat16, torch.float16):
+        for group in (32, 128):
+            steps = g.integers(-15, 16, (64, 512)).astype(np.float32)  # half steps: -7.5 .. 7.5
+            steps.reshape(64, -1, group)[:, :, 0], steps.reshape(64, -1, group)[:, :, 1] = -15, 15
+            w = torch.from_numpy(steps * np.float32(0.5) * g.choice([2.0 ** -6, 3 * 2.0 ** -9, 2.0 ** -3], (64, 1)).astype(
+                np.float32)).to(dtype)
+            for symmetric in (False, True):
+                gw = nf4.quantize_groups(w.cuda(), group, symmetric)
+                q, st, z = quantize_ref(w.float().numpy(), group, symmetric, dtype)
+                assert torch.equal(gw.scale.cpu(), st)
+                assert np.array_equal(gw.packed.cpu().numpy(), pack_ref(q))
+                assert symmetric or np.array_equal(gw.zero.cpu().numpy(), z)
+
+
+def test_groups_side_stream_argument():
+    w = torch.randn(64, 256, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gw = nf4.quantize_groups(w, 64, stream=side)
+    v = nf4.dequantize_groups(gw, stream=side)
+    x = torch.ones(2, 256, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.current_stream().synchronize()
+    y = nf4.gemv_groups(gw, x, stream=side)
+    side.synchronize()
+    assert torch.equal(v.double(), weight_values(gw))
+    check_gemv(gw, x, y)
+
+
 def test_quantize_groups_then_product():
     """a weight through quantize, its values and the decode product: the product uses exactly the expanded values"""
     w = torch.from_numpy(group_weights(300, 1024, 77)).cuda()
