@@ -11,7 +11,7 @@
 // The order of k inside an MMA is free as long as both operands use the same one: a word's pairs (0,1), (2,3) feed one
 // MMA and (4,5), (6,7) the next, against 16 contiguous bytes of x.
 //
-// The kernel lives on bytes in flight: each warp keeps kDepth steps of codes (1 KB each) loading in registers, and the
+// The kernel lives on bytes in flight: each warp keeps two steps of codes (1 KB each) loading in registers, and the
 // scales of the tile's 16 rows -- contiguous in memory -- come as one coalesced copy into shared memory, already
 // widened to (fp32 scale, packed bias + zero point), 256 groups at a time.
 // The warps' sums are added in a fixed order, so results are deterministic.
@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_step(uint32_t (&w)[2][4], const uint8_t* __
   }
 }
 
-template <bool kHalf, int kGroup, bool kZeros, int kWarps, int kDepth>
+template <bool kHalf, int kGroup, bool kZeros, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32)
     gemv_groups_kernel(const uint8_t* __restrict__ packed, const uint16_t* __restrict__ scale,
                        const uint8_t* __restrict__ zero, int64_t rows, int64_t cols, const uint16_t* __restrict__ x,
@@ -84,74 +84,78 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t r0 = tile + g;
   // rows past the last one read it again; they are not written
   const int64_t ra = r0 < rows ? r0 : rows - 1, rb = r0 + 8 < rows ? r0 + 8 : rows - 1;
-  const int groups = (int)(cols / kGroup), nsteps = (groups + kSub - 1) / kSub;
-  // a warp takes two neighbouring steps at a time (128 bytes of a row, a whole cache line), the warps in turn
-  auto step_of = [&](int i) { return ((i >> 1) * kWarps + warp) * 2 + (i & 1); };
-  const int full = nsteps / (2 * kWarps), rest = nsteps - full * 2 * kWarps - 2 * warp;
-  const int mine = 2 * full + (rest <= 0 ? 0 : rest == 1 ? 1 : 2);  // steps of this warp
-  const uint8_t* p0 = packed + ra * (cols / 2);
-  const uint8_t* p1 = packed + rb * (cols / 2);
+  const int groups = (int)(cols / kGroup);
+  // A warp takes two neighbouring steps at a time (128 bytes of a row, a whole cache line), the warps in turn.  Its
+  // pointers move on by a constant from pair to pair.
+  constexpr int kPair = 2 * kStep, kTurn = kWarps * kPair;  // columns per pair, per turn of all warps
+  const uint8_t* p0 = packed + ra * (cols / 2) + warp * (kPair / 2);
+  const uint8_t* p1 = packed + rb * (cols / 2) + warp * (kPair / 2);
+  int left = (int)cols - warp * kPair;  // columns from the pair's first one to the row's end (of the pair loaded next)
   // lanes past the batch read its last row again: their columns of the product are not written
-  const uint16_t* xr = x + (int64_t)(g < batch ? g : batch - 1) * cols + 8 * slot_word<kGroup>(0, t);
-  uint32_t buf[kDepth][2][4];
-  auto load = [&](int i, uint32_t (&w)[2][4]) {
-    const int st = step_of(i), off = st * (kStep / 2);
-    load_step<kGroup>(w, p0 + off, p1 + off, (int)cols - st * kStep, t);
+  const uint16_t* xr = x + (int64_t)(g < batch ? g : batch - 1) * cols + 8 * slot_word<kGroup>(0, t) + warp * kPair;
+  uint32_t buf[2][2][4];
+  auto load = [&](int d) {
+    if (d * kStep < left) load_step<kGroup>(buf[d], p0 + d * (kStep / 2), p1 + d * (kStep / 2), left - d * kStep, t);
   };
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d)
-    if (d < mine) load(d, buf[d]);
+  load(0);
+  load(1);
 
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kPerChunk = kChunk / kSub / kWarps;  // steps per warp and chunk
-  static_assert(kPerChunk % kDepth == 0 && kPerChunk % 2 == 0 && kPerChunk > 0, "chunks hold whole rounds");
-  for (int c = 0; c * kChunk < groups; ++c) {
-    const int gn = groups - c * kChunk < kChunk ? groups - c * kChunk : kChunk;
+  constexpr int kPerChunk = kChunk / (2 * kSub) / kWarps;  // pairs per warp and chunk of scales
+  static_assert(kPerChunk > 0, "chunk");
+  for (int c = 0; c < groups; c += kChunk) {
+    const int gn = groups - c < kChunk ? groups - c : kChunk;
     if (c > 0) __syncthreads();
     for (int i = threadIdx.x; i < 16 * gn; i += kWarps * 32) {
       const int r = i / gn, j = i - r * gn;
-      const int64_t at = (tile + r < rows ? tile + r : rows - 1) * groups + c * kChunk + j;
+      const int64_t at = (tile + r < rows ? tile + r : rows - 1) * groups + c + j;
       const float z = G::kBiasF + (kZeros ? (float)__ldg(zero + at) : 8.0f);
       meta[r * pitch + j] = make_float2(G::to_f32(__ldg(scale + at)), __uint_as_float(G::pack(z, z)));
     }
     __syncthreads();
-    const int end = (c + 1) * kPerChunk < mine ? (c + 1) * kPerChunk : mine;
-    for (int i0 = c * kPerChunk; i0 < end; i0 += kDepth) {
+    const float2* mp = meta + g * pitch + warp * (2 * kSub);
+    int gl = gn - warp * (2 * kSub);  // groups of the chunk from the pair's first one on
+#pragma unroll 1
+    for (int q = 0; q < kPerChunk && gl > 0; ++q) {
+      p0 += kTurn / 2;
+      p1 += kTurn / 2;
+      left -= kTurn;
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int i = i0 + d;
-        if (i >= end) break;
-        const int k0 = step_of(i) * kStep;
-        const int j0 = step_of(i) * kSub - c * kChunk;  // first group of the step within the chunk
+      for (int d = 0; d < 2; ++d) {
+        if (d * kSub < gl) {
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) {
-          if (kGroup < 128 && j0 + j >= gn) break;  // the last step may be short by whole groups
-          const float2 m0 = meta[g * pitch + j0 + j], m1 = meta[(g + 8) * pitch + j0 + j];
-          const uint32_t z0 = __float_as_uint(m0.y), z1 = __float_as_uint(m1.y);
-          float part[4];
+          for (int j = 0; j < kSub; ++j) {
+            if (kSub > 1 && d * kSub + j >= gl) break;  // the last step may be short by whole groups
+            const float2 m0 = mp[d * kSub + j], m1 = mp[8 * pitch + d * kSub + j];
+            const uint32_t z0 = __float_as_uint(m0.y), z1 = __float_as_uint(m1.y);
+            float part[4];
 #pragma unroll
-          for (int s = j * kSlots; s < (j + 1) * kSlots; ++s) {
-            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + k0 + 8 * (slot_word<kGroup>(s, 0))));
-            uint32_t a[2][4];
+            for (int s = j * kSlots; s < (j + 1) * kSlots; ++s) {
+              const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + d * kStep + 8 * slot_word<kGroup>(s, 0)));
+              uint32_t a[2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = buf[d][h][s], z = h ? z1 : z0;
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w = buf[d][h][s], z = h ? z1 : z0;
 #pragma unroll
-              for (int p = 0; p < 4; ++p) a[h][p] = G::sub2(nibbles_or(w >> (4 * p), bias), z);
+                for (int p = 0; p < 4; ++p) a[h][p] = G::sub2(nibbles_or(w >> (4 * p), bias), z);
+              }
+              if (s == j * kSlots)
+                G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+              else
+                G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, part[0], part[1], part[2], part[3]);
+              G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w, part[0], part[1], part[2], part[3]);
             }
-            if (s == j * kSlots)
-              G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
-            else
-              G::mma(part, a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y, part[0], part[1], part[2], part[3]);
-            G::mma(part, a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w, part[0], part[1], part[2], part[3]);
+            acc[0] = fmaf(m0.x, part[0], acc[0]);
+            acc[1] = fmaf(m0.x, part[1], acc[1]);
+            acc[2] = fmaf(m1.x, part[2], acc[2]);
+            acc[3] = fmaf(m1.x, part[3], acc[3]);
           }
-          acc[0] = fmaf(m0.x, part[0], acc[0]);
-          acc[1] = fmaf(m0.x, part[1], acc[1]);
-          acc[2] = fmaf(m1.x, part[2], acc[2]);
-          acc[3] = fmaf(m1.x, part[3], acc[3]);
         }
-        if (i + kDepth < mine) load(i + kDepth, buf[d]);
+        load(d);
       }
+      xr += kTurn;
+      mp += kWarps * 2 * kSub;
+      gl -= kWarps * 2 * kSub;
     }
   }
   // accumulator fragment: (row g, batch 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-template <bool kHalf, int kGroup, int kWarps, int kDepth>
+template <bool kHalf, int kGroup, int kWarps>
 cudaError_t launch_shape(const GroupWeight& w, const void* x, int batch, void* y, cudaStream_t stream) {
   static_assert(kWarps * 32 >= 16 * 8, "a thread per output of the tile");
   const dim3 grid((unsigned)((w.rows + 15) / 16)), block(kWarps * 32);
@@ -182,9 +186,9 @@ cudaError_t launch_shape(const GroupWeight& w, const void* x, int batch, void* y
   const size_t smem = (size_t)16 * pitch * sizeof(float2);
   const cudaError_t e =
       w.zero != nullptr
-          ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true, kWarps, kDepth>, grid, block, smem, stream, w.packed,
+          ? launch_pdl(gemv_groups_kernel<kHalf, kGroup, true, kWarps>, grid, block, smem, stream, w.packed,
                        scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch)
-          : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false, kWarps, kDepth>, grid, block, smem, stream, w.packed,
+          : launch_pdl(gemv_groups_kernel<kHalf, kGroup, false, kWarps>, grid, block, smem, stream, w.packed,
                        scale, w.zero, w.rows, w.cols, xs, batch, ys, pitch);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -195,8 +199,8 @@ cudaError_t launch(const GroupWeight& w, const void* x, int batch, void* y, cuda
   // Few tiles: sixteen warps share a tile's columns (4096x14336 batch 1: 11.6 us against 14.0 with eight).  Many: eight,
   // so that more tiles are under way on an SM (14336x4096 batch 1: 12.6 us against 13.8, batch 8 in groups of 64: 15.9
   // against 18.2).
-  return (w.rows + 15) / 16 <= 2 * (int64_t)num_sms ? launch_shape<kHalf, kGroup, 16, 2>(w, x, batch, y, stream)
-                                                    : launch_shape<kHalf, kGroup, 8, 2>(w, x, batch, y, stream);
+  return (w.rows + 15) / 16 <= 2 * (int64_t)num_sms ? launch_shape<kHalf, kGroup, 16>(w, x, batch, y, stream)
+                                                    : launch_shape<kHalf, kGroup, 8>(w, x, batch, y, stream);
 }
 
 template <bool kHalf>
