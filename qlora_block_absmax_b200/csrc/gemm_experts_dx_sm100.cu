@@ -482,7 +482,7 @@ cudaError_t launch_book(const ExpertsCall& c, const Maps& m, bool pair, int grid
 }  // namespace
 
 cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
-  const bool pair = experts_pair(c.m, c.experts);
+  const bool pair = experts_pair(c.m, c.experts, c.cols, c.rows, num_sms);
   const bool dq = c.scales.absmax == nullptr;
   const int64_t rb = c.cols / kBlock, stack = c.rows * c.experts;
   Maps m;

@@ -489,7 +489,7 @@ cudaError_t launch_form(const ExpertsCall& c, const CUtensorMap& xbig, const CUt
 }  // namespace
 
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms) {
-  const bool pair = experts_pair(c.m, c.experts);
+  const bool pair = experts_pair(c.m, c.experts, c.rows, c.cols, num_sms);
   CUtensorMap xbig, x16, wmap;
   if (!make_map(&xbig, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.in, c.cols, c.m, kHalfK,
                 pair ? Cfg<true>::kRowsB : Cfg<false>::kRowsB, CU_TENSOR_MAP_SWIZZLE_128B) ||

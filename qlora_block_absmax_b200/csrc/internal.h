@@ -171,8 +171,18 @@ struct ExpertsCall {
   void* out;           // [m, rows], or [m, cols]
   void* workspace;     // experts_workspace_bytes, or null when that is 0
 };
-// CTA pairs with tiles of 256 rows for more than 64 rows per expert on average, else tiles of 64 rows
-inline bool experts_pair(int64_t m, int experts) { return m > 64 * (int64_t)experts; }
+// CTA pairs with tiles of 256 rows, or CTAs alone with tiles of 64?  A stage costs about the same in either (it is the
+// decode of 128 weight rows per CTA), so the rounds over the SMs decide, for rows spread evenly over the experts; alone,
+// the last round can be split (where the reduction is long enough) and counts by its share.  2 experts of 256x4096, 1000
+// rows: 4 pair units are one round, 32 units alone, split, a quarter of one (25.0 against 16.8 us).
+inline bool experts_pair(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
+  const int64_t each = (m + experts - 1) / experts;
+  if (each <= 64) return false;
+  const int64_t alone = experts * ((each + 63) / 64) * (out_cols / 128);
+  const int64_t pairs = experts * ((each + 255) / 256) * ((out_cols + 255) / 256), workers = num_sms > 1 ? num_sms / 2 : 1;
+  const int64_t rounds = (pairs + workers - 1) / workers;
+  return reduction < 1024 ? rounds <= (alone + num_sms - 1) / num_sms : rounds * num_sms <= alone;
+}
 // Split reductions (tiles of 64 rows only): arrival counters, then one fp32 accumulator per item, at most kExpertsItems
 // items per SM.
 constexpr int kExpertsMaxSplit = 8;
@@ -181,7 +191,7 @@ constexpr size_t kExpertsCountBytes = 4096;  // fewer split units than SMs, 4 co
 inline size_t experts_partial_bytes(int64_t m) { return m > 32 ? 64 * 128 * 4 : 32 * 128 * 4; }
 inline size_t experts_workspace_bytes(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
   // no split is worth its exchange where a unit is short, and little where even the fewest possible units make many rounds
-  if (experts_pair(m, experts) || reduction < 1024 || num_sms > 255) return 0;
+  if (reduction < 1024 || num_sms > 255 || experts_pair(m, experts, out_cols, reduction, num_sms)) return 0;
   if ((m + 63) / 64 * (out_cols / 128) > 8 * (int64_t)num_sms) return 0;
   return kExpertsCountBytes + (size_t)kExpertsItems * num_sms * experts_partial_bytes(m);
 }

@@ -141,6 +141,43 @@ def test_pairs_at_odd_widths(out_cols, red, gradient):
     nf4.check_device_error()
 
 
+@pytest.mark.parametrize("out_cols,red", [(2176, 64), (2176, 192), (1664, 1088), (4224, 1024)])
+@pytest.mark.parametrize("gradient", [False, True])
+def test_pairs_on_a_full_gpu(out_cols, red, gradient):
+    """enough tiles that pairs are taken: a last column tile of 128, odd reductions, ragged tiles, experts without rows"""
+    counts = [257, 1, 0, 130, 512, 31, 700, 256]
+    n, k = (red, out_cols) if gradient else (out_cols, red)
+    qw, wc = make_stack(len(counts), n, k, seed=6)
+    off = offsets_of(counts, lead=3)
+    x = activations(sum(counts) + 5, n if gradient else k, 20)
+    f = nf4.gemm_experts_dx if gradient else nf4.gemm_experts
+    out = torch.full((x.shape[0], out_cols), 3.5, dtype=torch.bfloat16, device="cuda")
+    f(qw, x, off, len(counts), out=out)
+    check(out, *reference(wc, x, off, gradient), red)
+    assert bool((out[:3] == 3.5).all()) and bool((out[-2:] == 3.5).all())
+    for _ in range(3):
+        assert torch.equal(f(qw, x, off, len(counts), out=out.clone()), out)
+    nf4.check_device_error()
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("counts", [[1000, 1], [300, 300], [0, 129]])
+def test_many_rows_few_tiles(gradient, counts):
+    """many rows but a narrow output: tiles of one CTA, split over the reduction; a workspace too small is refused"""
+    n, k = (4096, 256) if gradient else (256, 4096)
+    qw, wc = make_stack(2, n, k, seed=7)
+    off = offsets_of(counts)
+    x = activations(sum(counts), n if gradient else k, 21)
+    f = nf4.gemm_experts_dx if gradient else nf4.gemm_experts
+    y = f(qw, x, off, 2)
+    check(y, *reference(wc, x, off, gradient), n if gradient else k)
+    for _ in range(5):
+        assert torch.equal(f(qw, x, off, 2), y)
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        f(qw, x, off, 2, workspace=torch.zeros(1024, dtype=torch.uint8, device="cuda"))
+    nf4.check_device_error()
+
+
 def test_side_stream_argument():
     """stream=: the output is allocated and written on that stream"""
     qw, wc = make_stack(2, 128, 128)
