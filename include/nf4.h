@@ -354,7 +354,9 @@ NF4_API size_t nf4_gemm_dx_workspace_bytes(const nf4_weight *w, int64_t m);
  *   workspace  device scratch of nf4_gemm_experts_workspace_bytes(w, experts,
  *            m) bytes, with nf4_gemm's contract (may be NULL when 0;
  *            zero-filled before its first use, left ready by every completed
- *            call; separate buffers for calls that may overlap). */
+ *            call; separate buffers for calls that may overlap).  The size
+ *            does not grow with m: a buffer for several sizes takes the
+ *            largest of theirs. */
 #define NF4_EXPERTS_MAX 256
 NF4_API nf4_status nf4_gemm_experts(const nf4_weight *w, int32_t experts, const void *x, const int32_t *offsets,
                                     int64_t m, void *y, void *workspace, size_t workspace_bytes,
