@@ -15,6 +15,11 @@
 // scales of the tile's 16 rows -- contiguous in memory -- come as one coalesced copy into shared memory, already
 // widened to (fp32 scale, packed bias + zero point), 256 groups at a time.
 // The warps' sums are added in a fixed order, so results are deterministic.
+//
+// Measured (cold weights): 14336x4096 batch 1, groups of 128 12.1 us (2.5 TB/s, 39 % of the measured copy bandwidth);
+// the loads alone take 7.3 us of it, the extraction of the codes some 100 ALU operations per 2048 weights and warp.
+// 4096x14336 fp16 11.3 us, 14336x4096 batch 8 in groups of 64 15.5 us, 32003x4128 in groups of 32 36 us; 1024x4096 4.1 us,
+// most of it launch and latency.
 #include "group.cuh"
 #include "internal.h"
 
