@@ -9,11 +9,12 @@
 // One lane holds two packed words (16 codes), G / 16 lanes share a group and find its range with shuffles.  The kernel's
 // bound is its instructions, so little is divided and nothing goes through the conversion units (a quarter of the rate of
 // the others): the quotients are products with an approximate 1 / s, rounded by adding 1.5 * 2^23.  Such a product is off
-// by less than 3e-6 (|w / s| <= 16); one that comes within that of a rounding border b (an integer and a half) is settled
-// exactly, so every code is the one the division gives:
+// by at most 1.5 * 2^-23 of its size, 2.9e-6 where |w / s| <= 16, and the fp32 quotient by 2^-24, 4.8e-7 below 16; a
+// product within 4e-6 of a rounding border b (an integer and a half) is settled exactly, so every code is the one the
+// division gives:
 //   fp32 source    by the division itself (2 in 10^5 values)
 //   16-bit source  w and b s have at most 11 and 16 significant bits, so where they differ, they do by 2^-16 of their
-//                  size, more than the distance: w / s = b, and the even neighbour is the code.  (w = s / 2 is common among
+//                  size, 7.6e-6 at the least border: w / s = b, and the even neighbour is the code.  (w = s / 2 is common among
 //                  bf16 weights: most warps meet a tie.)
 // 4096x4096 bf16 with zero points took 23.4 us with IEEE quotients, rintf and float-to-integer conversions on one word
 // per lane, 19.6 us with the division in every tie.
@@ -27,9 +28,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to the nearest integer, ties to even
-constexpr float kNear = 0.499997f;     // |t - rint(t)| beyond this: t may stand for a value on the other side of a border
+constexpr float kNear = 0.499996f;     // |t - rint(t)| beyond this: t may stand for a value on the other side of a border
 
-// t = w / s but for an error below 3e-6, q = rint(t): rint of the exact quotient where a near one is a tie
+// t = w / s but for an error below 4e-6, q = rint(t): rint of the exact quotient where a near one is a tie
 __device__ __forceinline__ float settle_tie(float t, float q) {
   const float d = t - q;
   // q's parity is the last mantissa bit of 1.5 * 2^23 + q
