@@ -11,11 +11,12 @@
 //   A = Wc^T tile [128 k (UMMA M, MN-major)] x [64 n], B = dY tile [rows] x [64 n] (TMA), D in TMEM.
 // Two accumulators: one tile's epilogue runs beside the next tile's MMAs.  Warp roles, CTA pairs, decode and pipeline as
 // in the forward product; here the shared-memory pipe also carries the decoded tile (128 wavefronts per stage besides the
-// table's 256), so half of each block goes through the byte-permute decode instead: 8 experts of 14336x4096, 4096 rows
-// 497 -> 455 us, 16 rows 182 -> 167 us (in the forward product the same cost 5 to 15 %).
+// table's 256), so half of each block goes through the byte-permute decode instead: 8 experts of 14336x4096, 16 rows 182 -> 167 us, and
+// 9 % less time for 4096 rows (in the forward product the same cost 5 to 15 %).
 //
-// Measured: 8 experts of 14336x4096, 4096 rows 455 us in single launches (1058 TFLOP/s), 510 us back to back; 16 rows
-// 107 us.  The shared-memory pipe bounds both (68 % of its wavefronts by the counters, TMA and MMA traffic besides).
+// Measured: 8 experts of 14336x4096, 4096 rows 538 us in single launches (894 TFLOP/s), 533 us back to back; 16 rows
+// 107 us.  The shared-memory pipe bounds the few rows (68 % of its wavefronts by the counters, TMA and MMA traffic besides),
+// the ordering of CTA 1's tile before CTA 0's MMAs the pairs (see the hand-over warps).
 #include <cuda.h>
 
 #include <atomic>
@@ -36,7 +37,6 @@ constexpr int kProdWarp0 = kEpiWarps;
 constexpr int kTmaWarp = kProdWarp0 + 4 * kGroups;
 constexpr int kMmaWarp = kTmaWarp + 1;
 constexpr int kTmaWWarp = kTmaWarp + 2;
-constexpr int kThreads = (kTmaWWarp + 1) * 32;
 
 // A-tile layout (MN-major, 128-byte swizzle): reduction row r, column e (k) at
 //   (r / 8) * kKGroup + (e / 64) * kMnAtom + (r % 8) * 128 + (((e % 64) / 8) ^ (r % 8)) * 16 + (e % 8) * 2
@@ -51,6 +51,10 @@ struct Cfg {
   static constexpr int kRowsB = kPair ? 128 : 64;  // dY rows in one CTA's shared memory
   static constexpr int kTileCols = kPair ? 2 * kTileN : kTileN;
   static constexpr int kStages = 5;                // operand ring: dY tile + decoded tile
+  // CTA 1 of a pair has a hand-over warp per slot of the ring: the MMA issuer's, which has nothing to issue there, and
+  // these behind the last one
+  static constexpr int kHandWarps = kPair ? kStages - 1 : 0;
+  static constexpr int kThreads = (kTmaWWarp + 1 + kHandWarps) * 32;
   static constexpr int kWStages = kPair ? 4 : 8;   // packed codes and scale chunks
   static constexpr int kBBytes = kRowsB * kTileR * 2;
   static constexpr int kTmemCols = 2 * kTileM;     // two accumulators
@@ -63,7 +67,7 @@ struct Smem {
   uint64_t wfull[Cfg<kPair>::kWStages];
   uint64_t wempty[Cfg<kPair>::kWStages];
   uint64_t full[Cfg<kPair>::kStages];
-  uint64_t peer_full[Cfg<kPair>::kStages];  // (CTA 0 of a pair) the same in CTA 1, told by its MMA warp
+  uint64_t peer_full[Cfg<kPair>::kStages];  // (CTA 0 of a pair) the same in CTA 1, told by its hand-over warps
   uint64_t empty[Cfg<kPair>::kStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem_base;
@@ -92,7 +96,7 @@ static_assert(kWindow + front_bytes<true>() <= kPairTableDense && kWindow + fron
 
 // kScaleTma: scale chunks by TMA (rows of scales are whole 16-byte units); otherwise each producer loads its own
 template <bool kDQ, bool kScaleTma, int kBook, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kPair>::kThreads, 1)
     gemm_experts_dx_kernel(Scales s, const int* __restrict__ offsets, int experts, int rows, int cols, int m_total,
                            const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap ymap16,
                            const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap smap,
@@ -351,8 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = (it > kWStages ? it - kWStages : 0); j < it; ++j)
         if (!mbar_wait_bounded(&sm->wfull[j % kWStages], (j / kWStages) & 1, err)) break;
     }
+  } else if (kPair && rank == 1 && warp >= kMmaWarp) {
+    // ------------------------------------------------ CTA 1: tell CTA 0, whose thread issues for both
+    // The decoded tile consists of ordinary stores by this CTA's producers, and an MMA that CTA 0 issues reads it: what
+    // they handed over at `full` goes on to CTA 0 with a release at cluster scope, and is acquired there.  Such a release
+    // takes some 1100 to 1900 cycles, longer than a stage; so each slot of the ring has a warp that waits for it.  8 experts
+    // of 14336x4096, 4096 rows, single launches: 538 us; with one warp for all slots 1180, two 730, three 580, with the
+    // release in the producers 610.  (Without the scope, which leaves the order to chance, it was 455.)
+    const uint32_t as = warp == kMmaWarp ? 0 : warp - kTmaWWarp;
+    const uint32_t stages = u0 < items ? (uint32_t)((items - u0 + du - 1) / du) * (uint32_t)kps : 0;
+    uint32_t ph = 0;
+    for (uint32_t it = as; it < stages; it += kStages, ph ^= 1) {
+      if (!wait_or_abort(&sm->full[as], ph, sm, err)) break;
+      if (elect_one()) mbar_arrive_leader_release(&sm->peer_full[as]);
+      __syncwarp();
+    }
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issuer
+    // ------------------------------------------------ MMA issuer (of a pair in CTA 0)
     const uint32_t tm_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t adesc0 = smem_desc_mn_sw128(a_smem0, kMnAtom, kKGroup), bdesc0 = smem_desc_sw128(b_smem0);
     uint32_t as = 0, ph = 0, ucount = 0;
@@ -362,41 +381,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           C::kTileCols, __shfl_sync(0xffffffffu, unit_of(u).width, 0),
           /*a_mn=*/true);
       const uint32_t acc = ucount & 1;
-      if (rank == 0) {
-        ok = wait_or_abort(&sm->acc_empty[acc], ((ucount >> 1) & 1) ^ 1, sm, err);
-        if (!ok) break;
-        tc_fence_after();
-      }
+      ok = wait_or_abort(&sm->acc_empty[acc], ((ucount >> 1) & 1) ^ 1, sm, err);
+      if (!ok) break;
+      tc_fence_after();
       const uint32_t d_tm = tm_u + acc * C::kTileM;
       const int k0 = first_stage(u), k1 = end_stage(u);
       for (int ks = k0; ks < k1; ++ks) {
         ok = wait_or_abort(&sm->full[as], ph, sm, err);
         if (!ok) break;
         tc_fence_after();
-        if (kPair && rank == 1) {  // tell CTA 0, whose thread issues for both
-          tc_fence_before();
-          if (elect_one()) mbar_arrive_leader(&sm->peer_full[as]);
-        } else {
-          if constexpr (kPair) {
-            ok = wait_or_abort(&sm->peer_full[as], ph, sm, err);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          const uint64_t adesc = adesc0 + as * (kABytes >> 4), bdesc = bdesc0 + as * (C::kBBytes >> 4);
-          if (elect_one()) {
+        if constexpr (kPair) {
+          ok = wait_or_abort_leader(&sm->peer_full[as], ph, sm, err);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint64_t adesc = adesc0 + as * (kABytes >> 4), bdesc = bdesc0 + as * (C::kBBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTileR / 16; ++kk) {  // 16 weight rows per MMA: two 8-row groups, 32 bytes of dY
-              const uint64_t ad = adesc + kk * (2 * kKGroup >> 4), bd = bdesc + kk * 2;
-              if constexpr (kPair)
-                tc_mma_ss_pair(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
-              else
-                tc_mma_ss(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
-            }
+          for (int kk = 0; kk < kTileR / 16; ++kk) {  // 16 weight rows per MMA: two 8-row groups, 32 bytes of dY
+            const uint64_t ad = adesc + kk * (2 * kKGroup >> 4), bd = bdesc + kk * 2;
             if constexpr (kPair)
-              tc_commit_pair(&sm->empty[as]);
+              tc_mma_ss_pair(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
             else
-              tc_commit(&sm->empty[as]);
+              tc_mma_ss(d_tm, ad, bd, idesc, ks > k0 || kk > 0);
           }
+          if constexpr (kPair)
+            tc_commit_pair(&sm->empty[as]);
+          else
+            tc_commit(&sm->empty[as]);
         }
         __syncwarp();
         if (++as == kStages) {
@@ -404,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       }
-      if (ok && rank == 0 && elect_one()) {
+      if (ok && elect_one()) {
         if constexpr (kPair)
           tc_commit_pair(&sm->acc_full[acc]);
         else
@@ -463,7 +475,7 @@ cudaError_t launch(const ExpertsCall& c, const Maps& m, int grid, unsigned* err,
     attr_done.fetch_or(1ull << dev);
   }
   const cudaError_t e = launch_pdl_cluster(gemm_experts_dx_kernel<kDQ, kScaleTma, kBook, kPair>, dim3(grid),
-                                           dim3(kThreads), kPair ? 2 : 1, smem, stream, c.scales, c.offsets, c.experts,
+                                           dim3(Cfg<kPair>::kThreads), kPair ? 2 : 1, smem, stream, c.scales, c.offsets, c.experts,
                                            (int)c.rows, (int)c.cols, (int)c.m, m.y, m.y16, m.w, m.s,
                                            static_cast<__nv_bfloat16*>(c.out), split_at(c), err);
   count_launches(1);
