@@ -352,12 +352,14 @@ NF4_API size_t nf4_gemm_dx_workspace_bytes(const nf4_weight *w, int64_t m);
  *            as they were.  Values outside 0 .. m are held to that range;
  *            where offsets decrease, which rows are written is unspecified.
  *   workspace  device scratch of nf4_gemm_experts_workspace_bytes(w, experts,
- *            m) bytes, with nf4_gemm's contract (may be NULL when 0;
- *            zero-filled before its first use, left ready by every completed
- *            call; separate buffers for calls that may overlap).  The size
+ *            m) bytes (may be NULL when 0; separate buffers for calls that may
+ *            overlap).  Its first NF4_EXPERTS_COUNTER_BYTES bytes are
+ *            zero-filled before its first use and left zero by every completed
+ *            call; what lies behind them does not matter.  The size
  *            does not grow with m: a buffer for several sizes takes the
  *            largest of theirs. */
 #define NF4_EXPERTS_MAX 256
+#define NF4_EXPERTS_COUNTER_BYTES 4096
 NF4_API nf4_status nf4_gemm_experts(const nf4_weight *w, int32_t experts, const void *x, const int32_t *offsets,
                                     int64_t m, void *y, void *workspace, size_t workspace_bytes,
                                     nf4_stream_t stream);

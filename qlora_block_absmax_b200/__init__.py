@@ -409,13 +409,15 @@ def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offset
             _need_out(out, (m, owidth), x)
         if workspace is None:
             ws_bytes = size(d, experts, m)
-            if ws_bytes:
-                workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=x.device)  # zeroed once, then reusable
+            if ws_bytes:  # a buffer for this call: of it, only the counters have to be zero
+                workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
+                workspace[:_lib.NF4_EXPERTS_COUNTER_BYTES].zero_()
         elif not workspace.is_cuda or workspace.get_device() != x.get_device():
             raise ValueError("workspace must be on the weight's device")
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
         st = call(d, experts, x.data_ptr(), offsets.data_ptr(), m, out.data_ptr(),
-                  workspace.data_ptr() if workspace is not None else None,
-                  workspace.numel() * workspace.element_size() if workspace is not None else 0, _raw_stream(x, stream))
+                  workspace.data_ptr() if workspace is not None else None, ws_bytes, _raw_stream(x, stream))
         if st:
             _lib.check(st, what)
     return out

@@ -17,6 +17,7 @@ STATUS_NAMES = {0: "NF4_OK", 1: "NF4_ERR_INVALID_ARG", 2: "NF4_ERR_MISALIGNED", 
 NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 NF4_DQ_E4M3, NF4_DQ_INT8 = 0, 1
 NF4_QUANT_NF4, NF4_QUANT_FP4 = 0, 1
+NF4_EXPERTS_COUNTER_BYTES = 4096
 
 # every symbol include/nf4.h declares: name -> (restype, argtypes)
 P = ctypes.c_void_p

@@ -495,6 +495,7 @@ nf4_status nf4_selftest_wait_timeout(nf4_stream_t stream) {
 // products grouped by expert
 
 static_assert(NF4_EXPERTS_MAX == nf4::kMaxExperts, "expert limit");
+static_assert(NF4_EXPERTS_COUNTER_BYTES == nf4::kExpertsCountBytes, "arrival counters");
 
 namespace {
 
