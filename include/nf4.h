@@ -356,8 +356,8 @@ NF4_API size_t nf4_gemm_dx_workspace_bytes(const nf4_weight *w, int64_t m);
  *            overlap).  Its first NF4_EXPERTS_COUNTER_BYTES bytes are
  *            zero-filled before its first use and left zero by every completed
  *            call; what lies behind them does not matter.  The size
- *            does not grow with m: a buffer for several sizes takes the
- *            largest of theirs. */
+ *            is 0 for an m whose product needs none, and otherwise the same for
+ *            every m: a buffer of the size for m = 1 serves them all. */
 #define NF4_EXPERTS_MAX 256
 #define NF4_EXPERTS_COUNTER_BYTES 4096
 NF4_API nf4_status nf4_gemm_experts(const nf4_weight *w, int32_t experts, const void *x, const int32_t *offsets,

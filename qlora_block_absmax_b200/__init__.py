@@ -442,7 +442,8 @@ def gemm_experts(qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, ex
 
 
 def gemm_experts_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
-    """Scratch bytes nf4_gemm_experts needs for `m` rows in all (0 when none; not growing with m)."""
+    """Scratch bytes nf4_gemm_experts needs for `m` rows in all: 0 when none, else the same for every m (a buffer of the
+    size for m = 1 serves them all)."""
     d = qw.descriptor()
     return int(_lib.load().nf4_gemm_experts_workspace_bytes(ctypes.byref(d), experts, m))
 
@@ -456,7 +457,8 @@ def gemm_experts_dx(qw: QuantizedWeight, dy: torch.Tensor, offsets: torch.Tensor
 
 
 def gemm_experts_dx_workspace_bytes(qw: QuantizedWeight, experts: int, m: int) -> int:
-    """Scratch bytes nf4_gemm_experts_dx needs for `m` rows in all (0 when none; not growing with m)."""
+    """Scratch bytes nf4_gemm_experts_dx needs for `m` rows in all: 0 when none, else the same for every m (a buffer of the
+    size for m = 1 serves them all)."""
     d = qw.descriptor()
     return int(_lib.load().nf4_gemm_experts_dx_workspace_bytes(ctypes.byref(d), experts, m))
 

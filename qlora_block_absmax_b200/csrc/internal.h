@@ -188,12 +188,15 @@ inline bool experts_pair(int64_t m, int experts, int64_t out_cols, int64_t reduc
 constexpr int kExpertsMaxSplit = 8;
 constexpr int kExpertsItems = 4;
 constexpr size_t kExpertsCountBytes = 4096;  // fewer split units than SMs, 4 counters each
+// of one accumulator: up to 32 rows lie closer together
 inline size_t experts_partial_bytes(int64_t m) { return m > 32 ? 64 * 128 * 4 : 32 * 128 * 4; }
+// 0 where m rows are not split, else a size that does not depend on m (one buffer serves every m, and m = 1 is split where
+// any m is)
 inline size_t experts_workspace_bytes(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
   // no split is worth its exchange where a unit is short, and little where even the fewest possible units make many rounds
   if (reduction < 1024 || num_sms > 255 || experts_pair(m, experts, out_cols, reduction, num_sms)) return 0;
   if ((m + 63) / 64 * (out_cols / 128) > 8 * (int64_t)num_sms) return 0;
-  return kExpertsCountBytes + (size_t)kExpertsItems * num_sms * experts_partial_bytes(m);
+  return kExpertsCountBytes + (size_t)kExpertsItems * num_sms * experts_partial_bytes(64);
 }
 cudaError_t launch_gemm_experts(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);
 cudaError_t launch_gemm_experts_dx(const ExpertsCall& c, unsigned* err, cudaStream_t stream, int num_sms);

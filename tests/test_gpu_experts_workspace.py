@@ -56,3 +56,17 @@ def test_only_the_counters_have_to_be_zero(gradient, counts):
     assert bool((ws[:_lib.NF4_EXPERTS_COUNTER_BYTES] == 0).all())
     assert torch.equal(y, f(qw, x, off, 4, workspace=ws))
     nf4.check_device_error()
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+def test_a_buffer_sized_for_one_row_serves_every_m(gradient):
+    """one buffer, made for a single decoded row, for calls of other numbers of rows in turn"""
+    n, k = (4096, 512) if gradient else (512, 4096)
+    qw, wc = make_stack(4, n, k)
+    f, size = functions(gradient)
+    ws = torch.zeros(size(qw, 4, 1), dtype=torch.uint8, device="cuda")
+    for counts in ([0, 1, 0, 0], [8, 8, 8, 8], [9, 8, 8, 8], [64, 0, 0, 1], [1, 0, 0, 0], [200, 3, 90, 40], [2, 0, 33, 0]):
+        off = offsets_of(counts)
+        x = activations(sum(counts), 4096, 25)
+        check(f(qw, x, off, 4, workspace=ws), *reference(wc, x, off, gradient), 4096)
+    nf4.check_device_error()
