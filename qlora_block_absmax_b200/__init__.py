@@ -387,6 +387,15 @@ def gemm_dx_workspace_bytes(qw: QuantizedWeight, m: int) -> int:
     return int(_lib.load().nf4_gemm_dx_workspace_bytes(ctypes.byref(d), m))
 
 
+def _workspace_bytes(workspace: torch.Tensor, like: torch.Tensor) -> int:
+    """The bytes from the start of a caller's workspace on that the call may use."""
+    if not workspace.is_cuda or workspace.get_device() != like.get_device():
+        raise ValueError("workspace must be on the weight's device")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offsets: torch.Tensor, experts: int,
              width: int, owidth: int, out, workspace, stream) -> torch.Tensor:
     packed = qw.packed
@@ -412,10 +421,8 @@ def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offset
             if ws_bytes:  # a buffer for this call: of it, only the counters have to be zero
                 workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
                 workspace[:_lib.NF4_EXPERTS_COUNTER_BYTES].zero_()
-        elif not workspace.is_cuda or workspace.get_device() != x.get_device():
-            raise ValueError("workspace must be on the weight's device")
         else:
-            ws_bytes = workspace.numel() * workspace.element_size()
+            ws_bytes = _workspace_bytes(workspace, x)
         st = call(d, experts, x.data_ptr(), offsets.data_ptr(), m, out.data_ptr(),
                   workspace.data_ptr() if workspace is not None else None, ws_bytes, _raw_stream(x, stream))
         if st:

@@ -70,3 +70,24 @@ def test_a_buffer_sized_for_one_row_serves_every_m(gradient):
         x = activations(sum(counts), 4096, 25)
         check(f(qw, x, off, 4, workspace=ws), *reference(wc, x, off, gradient), 4096)
     nf4.check_device_error()
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+def test_workspace_refusals(gradient):
+    """what is too small, strided or elsewhere"""
+    n, k = (1024, 256) if gradient else (256, 1024)
+    qw, _ = make_stack(2, n, k, seed=9)
+    f, size = functions(gradient)
+    off, x = offsets_of([3, 4]), activations(7, 1024, 26)
+    need = size(qw, 2, 7)
+    ws = torch.zeros(2 * need, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        f(qw, x, off, 2, workspace=ws[:1].expand(need))
+    with pytest.raises(ValueError, match="contiguous"):
+        f(qw, x, off, 2, workspace=ws[::2])
+    with pytest.raises(ValueError, match="device"):
+        f(qw, x, off, 2, workspace=ws.cpu())
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        f(qw, x, off, 2, workspace=ws[:need - 16])
+    with pytest.raises(RuntimeError, match="MISALIGNED"):
+        f(qw, x, off, 2, workspace=ws[1:])
