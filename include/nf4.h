@@ -416,7 +416,8 @@ NF4_API nf4_status nf4_dequantize_groups(const nf4_group_weight *w, void *out, i
  * with fp32 sums; unlike nf4_gemv's, the weight is not rounded to 16 bits
  * before the product.
  *   x  device [batch, cols], y  device [batch, rows] (2-byte aligned), both of
- *   w->scale_dtype;  1 <= batch <= 8. */
+ *   w->scale_dtype;  1 <= batch <= 8.  Like every product here, a call with
+ *   nothing to sum (cols == 0) writes nothing. */
 NF4_API nf4_status nf4_gemv_groups(const nf4_group_weight *w, const void *x, int32_t batch, void *y,
                                    nf4_stream_t stream);
 

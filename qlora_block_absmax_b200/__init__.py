@@ -409,7 +409,9 @@ def _experts(call, size, what: str, qw: QuantizedWeight, x: torch.Tensor, offset
         raise ValueError("offsets must be int32 with experts + 1 entries")
     if x.dim() < 1 or x.shape[-1] != width:
         raise ValueError(f"the activations' last dimension must be {width}")
-    m = x.numel() // width if width else 0
+    if width == 0:
+        raise ValueError("the weight has no columns to sum over")
+    m = x.numel() // width
     with _on_device(x, stream):
         d = ctypes.byref(qw.descriptor())
         if out is None:
@@ -570,6 +572,8 @@ def gemv_groups(gw: GroupWeight, x: torch.Tensor, out=None, stream=None) -> torc
         st = _lib.load().nf4_gemv_groups(ctypes.byref(d), x.data_ptr(), batch, out.data_ptr(), _raw_stream(x, stream))
         if st:
             _lib.check(st, "nf4_gemv_groups")
+        if cols == 0:  # nothing to sum, and nothing that the library has written
+            out.zero_()
     return out
 
 
