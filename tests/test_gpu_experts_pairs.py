@@ -51,3 +51,16 @@ def test_gradient_hand_over(out_cols, red):
     """the decoded tile of CTA 1 goes to an MMA that CTA 0 issues: every output against fp64, equal bits on many calls"""
     qw, wc = make_stack(len(COUNTS), red, out_cols, seed=8)
     run_pairs(qw, wc, out_cols, red, True, 22, 40)
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("scales", ["plain", "e4m3", "int8"])
+@pytest.mark.parametrize("book", ["nf4", "fp4"])
+@pytest.mark.parametrize("out_cols,red", [(2176, 1024), (2048, 1088), (1792, 1024), (2176, 192)])
+def test_weight_forms_on_pairs(book, scales, gradient, out_cols, red):
+    """every kind of weight on CTA pairs.  Widths with and without a last column tile of 128; rows of scales that are whole
+    16-byte units and that are not, by the output's width (gradient: 2048 both, 1792 the fp32 scales only) and by the
+    reduction's (forward: 1024 codes 16 at a time)"""
+    n, k = (red, out_cols) if gradient else (out_cols, red)
+    qw, wc = make_stack(len(COUNTS), n, k, book, scales, seed=11)
+    run_pairs(qw, wc, out_cols, red, gradient, 27, 3)
