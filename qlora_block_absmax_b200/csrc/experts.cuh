@@ -33,7 +33,8 @@ struct Schedule {
 // accumulator goes to the workspace; each epilogue warp (32 columns) that finds itself the last of its unit adds all of
 // them in order and stores the rows.  Nobody waits for another CTA, so launches that share the GPU cannot block one
 // another.  (One row through each of two experts of 4096x14336: 58.9 -> 36 us; gradient of 16 rows, 8 experts of
-// 14336x4096: 161 -> 107 us.  Pairs gain nothing: a 256-row tile's exchange costs what the fuller round saves.)
+// 14336x4096: 161 -> 107 us.  Pairs are not split: in the forward product a 256-row tile's exchange cost what the fuller
+// round saved; the gradient's pairs, whose units are longer, were not tried.)
 constexpr int kMinSplitStages = 4;
 
 struct Split {

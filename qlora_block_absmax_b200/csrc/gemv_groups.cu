@@ -17,7 +17,8 @@
 // The warps' sums are added in a fixed order, so results are deterministic.
 //
 // Measured (cold weights): 14336x4096 batch 1, groups of 128 12.1 us (2.5 TB/s, 39 % of the measured copy bandwidth);
-// the loads alone take 7.3 us of it, the extraction of the codes some 100 ALU operations per 2048 weights and warp.
+// the loads alone take 7.3 us of it.  No pipe is full (57344x4096: ALU 54 %, L1 59 %, issue 58 %): a step's loads, the
+// extraction of its codes (7 ALU operations and 4 packed subtractions per word) and its MMAs wait for one another.
 // 4096x14336 fp16 11.3 us, 14336x4096 batch 8 in groups of 64 15.5 us, 32003x4128 in groups of 32 36 us; 1024x4096 4.1 us,
 // most of it launch and latency.
 #include "group.cuh"

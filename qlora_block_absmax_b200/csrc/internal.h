@@ -174,7 +174,9 @@ struct ExpertsCall {
 // CTA pairs with tiles of 256 rows, or CTAs alone with tiles of 64?  A stage costs about the same in either (it is the
 // decode of 128 weight rows per CTA), so the rounds over the SMs decide, for rows spread evenly over the experts; alone,
 // the last round can be split (where the reduction is long enough) and counts by its share.  2 experts of 256x4096, 1000
-// rows: 4 pair units are one round, 32 units alone, split, a quarter of one (25.0 against 16.8 us).
+// rows: 4 pair units are one round, 32 units alone, split, a quarter of one (25.0 against 16.8 us).  Where pairs are taken with
+// little to spare: 10 experts of 2048x4096, 128 rows each, 2 rounds of pairs against 320 units alone, 38 against 55 us (the
+// gradient of 4096x2048, whose pairs pay for their hand-over, 54 against 67).
 inline bool experts_pair(int64_t m, int experts, int64_t out_cols, int64_t reduction, int num_sms) {
   const int64_t each = (m + experts - 1) / experts;
   if (each <= 64) return false;
